@@ -1,0 +1,239 @@
+// One AdamW step over many tensors.
+//
+//   g' = g s,  m = b1 m + (1 - b1) g',  v = b2 v + (1 - b2) g'^2
+//   p  = p (1 - lr wd) - lr / (1 - b1^t) * m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+//
+// The tensors' addresses and sizes travel in the kernel's parameters, so a
+// call needs no device table and no copy.  A warp takes a block of 256
+// consecutive elements of one tensor, eight a lane: with 8-bit moments such a
+// block shares one scale for m and one for sqrt(v), which the warp finds and
+// applies without leaving its registers.  8-bit moments are E4M3 values of
+// m / scale and sqrt(v) / scale: sqrt(v) spans half of v's binades, so that
+// E4M3's seventeen reach v's from 1 down to 2^-34 of a block's largest.
+//
+// Each operation is rounded by itself (no contraction to fused multiply-adds),
+// so that the 8-bit codes are the same on every path and in any restatement
+// of the formulas in float32.
+
+#include <algorithm>
+#include <cmath>
+#include <memory>
+#include <new>
+
+#include "learn.cuh"
+#include "learn.h"
+
+namespace chol {
+namespace {
+
+constexpr int kBlock = 256;           // elements that share a scale
+constexpr int kWarps = 8;             // blocks of elements per thread block
+constexpr int kPerLane = kBlock / 32;
+
+struct Entry {
+    int64_t numel;
+    void* param;
+    const void* grad;
+    void* m;
+    void* v;
+    float* m_scale;
+    float* v_scale;
+    void* copy;
+    double decay;  // 1 - lr weight_decay
+};
+
+struct Scalars {
+    float beta1, rest1, beta2, rest2;  // b, 1 - b
+    float root;                        // 1 / sqrt(1 - b2^t)
+    float rate;                        // lr / (1 - b1^t)
+    float eps;
+    const float* grad_scale;
+    const int32_t* status;
+};
+
+// N entries and the first thread block of each (and, behind them, the number
+// of thread blocks).
+template <int N>
+struct Table {
+    Scalars s;
+    int32_t count;
+    uint32_t first[N + 1];
+    Entry e[N];
+};
+
+// The scale of a block whose largest magnitude is `top` (its bits; NaN stays).
+__device__ __forceinline__ float block_scale(uint32_t top) {
+    const float s = __fmul_rn(__uint_as_float(top), 1.0f / 448.0f);
+    return s < 0x1p-100f ? 0x1p-100f : s;
+}
+
+// One element: m, v and r = sqrt(v) updated, and the amount to subtract.
+__device__ __forceinline__ float adam(const Scalars& s, float g, float& m, float& v, float& r) {
+    m = __fadd_rn(__fmul_rn(m, s.beta1), __fmul_rn(g, s.rest1));
+    v = __fadd_rn(__fmul_rn(v, s.beta2), __fmul_rn(__fmul_rn(g, g), s.rest2));
+    r = __fsqrt_rn(v);
+    return __fmul_rn(__fdiv_rn(m, __fadd_rn(__fmul_rn(r, s.root), s.eps)), s.rate);
+}
+
+__device__ __forceinline__ float decayed(float p, double decay, float step) {
+    return __fsub_rn(__fmul_rn(p, (float)decay), step);
+}
+__device__ __forceinline__ double decayed(double p, double decay, float step) {
+    return __dsub_rn(__dmul_rn(p, decay), (double)step);
+}
+template <typename P> struct wide_of { using type = float; };
+template <> struct wide_of<double> { using type = double; };
+template <typename P, typename W> __device__ __forceinline__ P narrow(W x) {
+    if constexpr (sizeof(W) == 8) return x;
+    else return from_f32<P>(x);
+}
+template <typename P> __device__ __forceinline__ typename wide_of<P>::type widen(P x) {
+    if constexpr (sizeof(P) == 8) return x;
+    else return to_f32(x);
+}
+
+template <typename P, typename G, int BITS, int N>
+__global__ void __launch_bounds__(kWarps * 32)
+adamw_kernel(const __grid_constant__ Table<N> tab) {
+    if (tab.s.status != nullptr && *tab.s.status != 0) return;
+    // the entry with first[i] <= blockIdx.x < first[i + 1]
+    int lo = 0, hi = tab.count - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (tab.first[mid] <= blockIdx.x) lo = mid; else hi = mid - 1;
+    }
+    const Entry& e = tab.e[lo];
+    const int lane = threadIdx.x % 32;
+    const int64_t block = (int64_t)(blockIdx.x - tab.first[lo]) * kWarps + threadIdx.x / 32;
+    const int64_t at = block * kBlock;
+    if (at >= e.numel) return;
+    const int n = (int)min((int64_t)kBlock, e.numel - at);
+    const float gs = tab.s.grad_scale != nullptr ? *tab.s.grad_scale : 1.0f;
+    P* p = static_cast<P*>(e.param) + at;
+    const G* g = static_cast<const G*>(e.grad) + at;
+    G* copy = e.copy != nullptr ? static_cast<G*>(e.copy) + at : nullptr;
+    float m[kPerLane], v[kPerLane], r[kPerLane];
+    float ms = 0.0f, vs = 0.0f;
+    if constexpr (BITS == 8) ms = e.m_scale[block], vs = e.v_scale[block];
+    uint32_t mtop = 0, rtop = 0;
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i) {
+        const int j = i * 32 + lane;
+        m[i] = v[i] = r[i] = 0.0f;
+        if (j >= n) continue;
+        if constexpr (BITS == 8) {
+            m[i] = __fmul_rn(from_e4m3(static_cast<const uint8_t*>(e.m)[at + j]), ms);
+            r[i] = __fmul_rn(from_e4m3(static_cast<const uint8_t*>(e.v)[at + j]), vs);
+            v[i] = __fmul_rn(r[i], r[i]);
+        } else {
+            m[i] = static_cast<const float*>(e.m)[at + j];
+            v[i] = static_cast<const float*>(e.v)[at + j];
+        }
+        const float step = adam(tab.s, __fmul_rn(to_f32(g[j]), gs), m[i], v[i], r[i]);
+        const auto w = decayed(widen<P>(p[j]), e.decay, step);
+        p[j] = narrow<P>(w);
+        if constexpr (sizeof(G) == 2 && sizeof(P) == 4)
+            if (copy != nullptr) copy[j] = from_f32<G>(w);
+        mtop = max(mtop, abs_bits(m[i]));
+        rtop = max(rtop, abs_bits(r[i]));
+    }
+    if constexpr (BITS == 8) {
+        ms = block_scale(warp_max(mtop)), vs = block_scale(warp_max(rtop));
+        if (lane == 0) e.m_scale[block] = ms, e.v_scale[block] = vs;
+        ms = __frcp_rn(ms), vs = __frcp_rn(vs);
+    }
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i) {
+        const int j = i * 32 + lane;
+        if (j >= n) continue;
+        if constexpr (BITS == 8) {
+            float q = __fmul_rn(r[i], vs);
+            if (r[i] > 0.0f && q < 0x1p-9f) q = 0x1p-9f;  // a root above 0 stays above 0
+            static_cast<uint8_t*>(e.m)[at + j] = to_e4m3(__fmul_rn(m[i], ms));
+            static_cast<uint8_t*>(e.v)[at + j] = to_e4m3(q);
+        } else {
+            static_cast<float*>(e.m)[at + j] = m[i];
+            static_cast<float*>(e.v)[at + j] = v[i];
+        }
+    }
+}
+
+template <int N, typename P, typename G, int BITS>
+cudaError_t launch(int64_t count, const chol_adamw_tensor* t, const AdamwArgs& a,
+                   const Scalars& s, cudaStream_t stream) {
+    std::unique_ptr<Table<N>> tab(new (std::nothrow) Table<N>);
+    if (tab == nullptr) return cudaErrorMemoryAllocation;
+    tab->s = s;
+    constexpr int64_t kChunk = (int64_t)kBlock * kWarps;
+    constexpr uint64_t kMaxGrid = 0x7fffffff;
+    int64_t i = 0, done = 0;  // `done` thread blocks' worth of tensor i is launched already
+    while (i < count) {
+        uint64_t blocks = 0;
+        tab->count = 0;
+        while (i < count && tab->count < N && blocks < kMaxGrid) {
+            const int64_t from = done * kChunk;
+            if (t[i].numel <= from) {
+                ++i, done = 0;
+                continue;
+            }
+            const int64_t need = (t[i].numel - from + kChunk - 1) / kChunk;
+            const int64_t take = (int64_t)std::min<uint64_t>(need, kMaxGrid - blocks);
+            Entry& e = tab->e[tab->count];
+            e.numel = std::min<int64_t>(t[i].numel - from, take * kChunk);
+            e.param = static_cast<P*>(t[i].param) + from;
+            e.grad = static_cast<const G*>(t[i].grad) + from;
+            const int64_t state = from * (BITS / 8), block = from / kBlock;
+            e.m = static_cast<char*>(t[i].m) + state;
+            e.v = static_cast<char*>(t[i].v) + state;
+            e.m_scale = BITS == 8 ? t[i].m_scale + block : nullptr;
+            e.v_scale = BITS == 8 ? t[i].v_scale + block : nullptr;
+            e.copy = t[i].copy != nullptr ? static_cast<G*>(t[i].copy) + from : nullptr;
+            e.decay = 1.0 - a.lr * t[i].weight_decay;
+            tab->first[tab->count++] = (uint32_t)blocks;
+            blocks += take;
+            if (take == need) ++i, done = 0; else done += take;
+        }
+        if (tab->count == 0) break;
+        tab->first[tab->count] = (uint32_t)blocks;
+        adamw_kernel<P, G, BITS, N><<<(unsigned)blocks, kWarps * 32, 0, stream>>>(*tab);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+// Kernel parameters are at most 32,764 bytes: 360 entries.  A table that a few
+// tensors fit travels in 4 KB.
+template <typename P, typename G, int BITS>
+cudaError_t by_count(int64_t count, const chol_adamw_tensor* t, const AdamwArgs& a,
+                     const Scalars& s, cudaStream_t stream) {
+    return count <= 48 ? launch<48, P, G, BITS>(count, t, a, s, stream)
+                       : launch<360, P, G, BITS>(count, t, a, s, stream);
+}
+
+template <typename P, typename G>
+cudaError_t by_bits(int64_t count, const chol_adamw_tensor* t, const AdamwArgs& a,
+                    const Scalars& s, cudaStream_t stream) {
+    return a.state_bits == 8 ? by_count<P, G, 8>(count, t, a, s, stream)
+                             : by_count<P, G, 32>(count, t, a, s, stream);
+}
+
+}  // namespace
+
+cudaError_t adamw(int64_t count, const chol_adamw_tensor* t, const AdamwArgs& a,
+                  cudaStream_t stream) {
+    const double c1 = 1.0 - std::pow(a.beta1, (double)a.step);
+    const double c2 = 1.0 - std::pow(a.beta2, (double)a.step);
+    const Scalars s = {(float)a.beta1, (float)(1.0 - a.beta1), (float)a.beta2,
+                       (float)(1.0 - a.beta2), (float)(1.0 / std::sqrt(c2)), (float)(a.lr / c1),
+                       (float)a.eps, a.grad_scale, a.status};
+    if (a.param_dtype == CHOL_F64) return by_bits<double, double>(count, t, a, s, stream);
+    if (a.param_dtype == CHOL_F16) return by_bits<__half, __half>(count, t, a, s, stream);
+    if (a.param_dtype == CHOL_BF16)
+        return by_bits<__nv_bfloat16, __nv_bfloat16>(count, t, a, s, stream);
+    if (a.grad_dtype == CHOL_F16) return by_bits<float, __half>(count, t, a, s, stream);
+    if (a.grad_dtype == CHOL_BF16) return by_bits<float, __nv_bfloat16>(count, t, a, s, stream);
+    return by_bits<float, float>(count, t, a, s, stream);
+}
+
+}  // namespace chol

@@ -11,23 +11,20 @@
 #include "chol.h"
 #include "chol_tile.cuh"
 #include "chol_selftest.h"
+#include "checks.h"
 #include "common.cuh"
 #include "kernels.h"
 
 namespace {
 
+using chol::Range;
+using chol::aligned;
+using chol::is_device_pointer;
+using chol::overlaps;
+using chol::range_of;
+using chol::to_code;
+
 constexpr int kSmallMax = 64;
-
-struct Range {
-    uintptr_t lo, hi;  // [lo, hi)
-};
-
-bool overlaps(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
-
-Range range_of(const void* p, size_t bytes) {
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return Range{lo, lo + bytes};
-}
 
 int elem_size(int32_t dtype) {
     switch (dtype) {
@@ -44,19 +41,6 @@ using chol_tile::cplx;
 template <typename T> struct is_cplx : std::false_type {};
 template <typename R> struct is_cplx<cplx<R>> : std::true_type {};
 template <typename T> constexpr bool is_complex() { return is_cplx<T>::value; }
-
-// Device (or managed) memory only: a host pointer handed to a kernel would
-// fault or, where the GPU can reach host memory, silently run over the link.
-bool is_device_pointer(const void* p) {
-    cudaPointerAttributes attr;
-    if (cudaPointerGetAttributes(&attr, p) != cudaSuccess) {
-        cudaGetLastError();  // clear the non-sticky error
-        return false;
-    }
-    return attr.type == cudaMemoryTypeDevice || attr.type == cudaMemoryTypeManaged;
-}
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // Common shape / pointer checks.  On success *bytes is the size of one
 // [batch][n][n] array.
@@ -88,8 +72,6 @@ int pick_tile(int32_t tile, int n, int64_t batch, int esize, bool tensor_ok) {
     if (tensor_ok && n > 128 && batch * 8 <= chol::device_sm_count()) return 128;
     return std::min(chol::blocked_default_tile(n, batch), chol::blocked_max_tile(esize));
 }
-
-int to_code(cudaError_t e) { return e == cudaSuccess ? CHOL_OK : CHOL_ECUDA; }
 
 // f(T{}) for the element type of a (checked) dtype.
 template <typename F>

@@ -1,0 +1,94 @@
+// Device helpers of the operators for learning with the factor: element
+// conversions, vectors of elements, and reductions over warps and blocks.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "chol_learn.h"
+#include "common.cuh"
+
+namespace chol {
+
+// Model element types to and from float32 (to nearest even).
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f32(double x) { return __double2float_rn(x); }
+
+template <typename T> __device__ __forceinline__ T from_f32(float x);
+template <> __device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <> __device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
+    return __float2bfloat16_rn(x);
+}
+
+// |x| as an unsigned integer: ordered as the numbers are, with infinity above
+// them and NaN above that, so that an integer maximum keeps a NaN and does
+// not depend on the order of its operands.
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+// 8-bit codes.  E4M3: to nearest even, values beyond 448 become 448, NaN
+// stays.  I8: to nearest even, held to +-127 (NaN becomes 0).
+__device__ __forceinline__ uint8_t to_e4m3(float x) {
+    return (uint8_t)__nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ uint8_t to_i8(float x) {
+    return (uint8_t)(int8_t)__float2int_rn(fminf(fmaxf(x, -127.0f), 127.0f));
+}
+__device__ __forceinline__ float from_e4m3(uint8_t q) {
+    const __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)q, __NV_E4M3);
+    return __half2float(__half(h));
+}
+
+template <typename T> struct type_tag {
+    using type = T;
+};
+
+// f(type_tag<T>{}) for a model type of chol_learn.h.
+template <typename F>
+cudaError_t model_dispatch(int32_t dtype, F&& f) {
+    switch (dtype) {
+        case CHOL_F32: return f(type_tag<float>{});
+        case CHOL_F16: return f(type_tag<__half>{});
+        case CHOL_BF16: return f(type_tag<__nv_bfloat16>{});
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+__device__ __forceinline__ uint32_t warp_max(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
+
+// Over a block of NT threads (a multiple of 32, at most 1024); every thread
+// gets the result.  `tmp` is 32 words of shared memory of its own.
+template <int NT>
+__device__ __forceinline__ float block_sum(float x, float* tmp) {
+    x = warp_sum(x);
+    if constexpr (NT > 32) {
+        if (threadIdx.x % 32 == 0) tmp[threadIdx.x / 32] = x;
+        __syncthreads();
+        x = threadIdx.x % 32 < NT / 32 ? tmp[threadIdx.x % 32] : 0.0f;
+        x = warp_sum(x);
+    }
+    return x;
+}
+template <int NT>
+__device__ __forceinline__ uint32_t block_max(uint32_t x, uint32_t* tmp) {
+    x = warp_max(x);
+    if constexpr (NT > 32) {
+        if (threadIdx.x % 32 == 0) tmp[threadIdx.x / 32] = x;
+        __syncthreads();
+        x = threadIdx.x % 32 < NT / 32 ? tmp[threadIdx.x % 32] : 0u;
+        x = warp_max(x);
+    }
+    return x;
+}
+
+}  // namespace chol

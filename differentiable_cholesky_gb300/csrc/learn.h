@@ -1,0 +1,87 @@
+// Internal launch interface of the operators for learning with the factor
+// (chol_learn.h): between learn_api.cu and the kernels.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "chol_learn.h"
+
+namespace chol {
+
+// ---- rmsnorm.cu ----------------------------------------------------------
+struct RmsArgs {
+    int64_t rows, d;
+    float eps;
+    int group;         // 8-bit output: 0 (rows) or 128 columns per scale
+    const void* x;     // at stride ldx
+    int64_t ldx;
+    const void* res;   // may be null; at stride ldr
+    int64_t ldr;
+    const void* w;     // may be null
+    void* y;
+    float* scale;      // 8-bit output only
+    void* r;           // may be null; may be res
+    float* rstd;       // may be null
+};
+// dtype / res_dtype / y_dtype: checked combinations of chol_learn.h.
+cudaError_t rms_norm(const RmsArgs& a, int32_t dtype, int32_t res_dtype, int32_t y_dtype,
+                     cudaStream_t stream);
+
+struct RmsAdjArgs {
+    int64_t rows, d;
+    const void* adj_y;  // at stride ldy
+    int64_t ldy;
+    const void* r;      // at stride ldr
+    int64_t ldr;
+    const void* w;      // may be null
+    const float* rstd;
+    const void* adj_r;  // may be null
+    void* adj_in;       // may be null; may be adj_r
+    void* adj_x;        // may be null
+    void* adj_w;        // may be null
+    float* work;        // rms_norm_adj_workspace_bytes()
+};
+size_t rms_norm_adj_workspace_bytes(int64_t rows, int64_t d);
+cudaError_t rms_norm_adj(const RmsAdjArgs& a, int32_t dtype, int32_t r_dtype,
+                         cudaStream_t stream);
+
+// ---- linrec.cu -----------------------------------------------------------
+struct LinrecArgs {
+    int64_t batch, time, d;
+    const void* g;
+    int64_t g_bs, g_ts;
+    const void* x;
+    int64_t x_bs, x_ts;
+    const float* state0;     // may be null
+    const int64_t* offsets;  // may be null
+    int64_t nseq;            // sequences (batch without offsets)
+    // forward
+    void* h;                 // the adjoint reads it
+    float* state1;           // may be null
+    // adjoint
+    const void* adj_h;
+    int64_t dh_bs, dh_ts;
+    const float* adj_s1;     // may be null
+    void* adj_g;
+    void* adj_x;
+    float* adj_s0;           // may be null
+    int32_t* status;         // may be null
+    void* work;              // linrec_workspace_bytes()
+};
+size_t linrec_workspace_bytes(int64_t batch, int64_t time, int64_t d, int32_t dtype);
+cudaError_t linrec(const LinrecArgs& a, int32_t dtype, int32_t gate, bool complement, bool adjoint,
+                   cudaStream_t stream);
+
+// ---- adamw.cu ------------------------------------------------------------
+struct AdamwArgs {
+    int32_t param_dtype, grad_dtype, state_bits;
+    double lr, beta1, beta2, eps;
+    int64_t step;
+    const float* grad_scale;  // may be null
+    const int32_t* status;    // may be null
+};
+cudaError_t adamw(int64_t count, const chol_adamw_tensor* tensors, const AdamwArgs& a,
+                  cudaStream_t stream);
+
+}  // namespace chol

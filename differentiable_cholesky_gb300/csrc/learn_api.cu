@@ -1,0 +1,407 @@
+// C entry points of the operators for learning with the factor
+// (chol_learn.h): argument checks and workspace handling.  No kernel code
+// lives here.
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <cmath>
+#include <initializer_list>
+#include <new>
+#include <vector>
+
+#include "checks.h"
+#include "chol_learn.h"
+#include "learn.h"
+
+namespace {
+
+using chol::aligned;
+using chol::is_device_pointer;
+using chol::overlaps;
+using chol::Range;
+using chol::range_of;
+using chol::to_code;
+
+typedef unsigned __int128 u128;
+
+constexpr u128 kMaxBytes = (u128)1 << 62;
+constexpr int64_t kMaxD = 1 << 30;  // columns and channels are 32-bit in the kernels
+
+// Bytes of an element of a model type (0: not one).
+size_t model_size(int32_t dtype) {
+    switch (dtype) {
+        case CHOL_F32: return 4;
+        case CHOL_F16:
+        case CHOL_BF16: return 2;
+        default: return 0;
+    }
+}
+
+// An argument in device memory, aligned to `align`.
+bool usable(const void* p, size_t align) {
+    return p != nullptr && aligned(p, align) && is_device_pointer(p);
+}
+bool usable_or_null(const void* p, size_t align) { return p == nullptr || usable(p, align); }
+
+// Bytes spanned by n rows of d elements at stride ld.
+u128 span(int64_t n, int64_t ld, int64_t d, size_t es) {
+    return n == 0 ? 0 : ((u128)(n - 1) * (u128)ld + (u128)d) * es;
+}
+
+// Memory that a call writes or reads (empty where the pointer is null).
+struct Use {
+    const void* p;
+    u128 bytes;
+    bool out;
+    const void* in_place;  // an input that this output may be, exactly
+};
+
+// No output overlaps an input or another output, but for one that is the
+// input it may replace.
+bool aliased(std::initializer_list<Use> uses) {
+    for (const Use& a : uses) {
+        if (!a.out || a.p == nullptr || a.bytes == 0) continue;
+        for (const Use& b : uses) {
+            if (&a == &b || b.p == nullptr || b.bytes == 0) continue;
+            if (!b.out && a.in_place != nullptr && a.p == b.p && a.in_place == b.p) continue;
+            if (overlaps(range_of(a.p, (size_t)a.bytes), range_of(b.p, (size_t)b.bytes)))
+                return true;
+        }
+    }
+    return false;
+}
+
+// The caller's workspace, or one taken on the stream for the call.
+class Work {
+  public:
+    explicit Work(cudaStream_t stream) : stream_(stream) {}
+    int get(void* given, int64_t given_bytes, size_t need, void** out) {
+        *out = given;
+        if (need == 0) return CHOL_OK;
+        if (given != nullptr) return (size_t)given_bytes >= need ? CHOL_OK : CHOL_ENOMEM;
+        if (cudaMallocAsync(&own_, need, stream_) != cudaSuccess) {
+            cudaGetLastError();
+            own_ = nullptr;
+            return CHOL_ENOMEM;
+        }
+        *out = own_;
+        return CHOL_OK;
+    }
+    int done(int rc) {
+        if (own_ != nullptr && cudaFreeAsync(own_, stream_) != cudaSuccess) return CHOL_ECUDA;
+        return rc;
+    }
+
+  private:
+    cudaStream_t stream_;
+    void* own_ = nullptr;
+};
+
+bool work_ok(const void* work, int64_t bytes) {
+    return work == nullptr || (bytes >= 0 && usable(work, 16));
+}
+
+// Shape and type checks of both recurrence calls.
+int check_linrec(int64_t batch, int64_t time, int64_t d, int32_t dtype, int32_t gate,
+                 int32_t complement, std::initializer_list<int64_t> bs,
+                 std::initializer_list<int64_t> ts, const int64_t* offsets, int64_t nseq) {
+    const size_t es = model_size(dtype);
+    if (es == 0) return CHOL_EDTYPE;
+    if (batch < 0 || time < 0 || d <= 0 || d > kMaxD) return CHOL_EINVAL;
+    if (gate < CHOL_GATE_LINEAR || gate > CHOL_GATE_LOGIT) return CHOL_EINVAL;
+    if (complement != 0 && complement != 1) return CHOL_EINVAL;
+    if ((u128)batch * (u128)time * (u128)d * 4 > kMaxBytes) return CHOL_EINVAL;
+    if (offsets != nullptr && (batch != 1 || nseq < 0 || (nseq == 0 && time > 0)))
+        return CHOL_EINVAL;
+    if ((u128)(offsets != nullptr ? nseq : batch) * (u128)d * 4 > kMaxBytes) return CHOL_EINVAL;
+    for (int64_t s : bs)
+        if (s < 0 || (u128)s * (u128)std::max<int64_t>(batch, 1) * es > kMaxBytes)
+            return CHOL_EINVAL;
+    for (int64_t s : ts)
+        if (s < 0 || (time > 1 && s < d) ||
+            (u128)s * (u128)std::max<int64_t>(time, 1) * es > kMaxBytes)
+            return CHOL_EINVAL;
+    return CHOL_OK;
+}
+
+// Bytes spanned by a [batch][time][d] array with strides.
+u128 span3(int64_t batch, int64_t bs, int64_t time, int64_t ts, int64_t d, size_t es) {
+    if (batch == 0 || time == 0) return 0;
+    return ((u128)(batch - 1) * bs + (u128)(time - 1) * ts + d) * es;
+}
+
+// float[rows][d] copied, or zeros, where a recurrence has no steps.
+int copy_states(const float* from, float* to, int64_t rows, int64_t d, int32_t* status,
+                cudaStream_t s) {
+    const size_t bytes = (size_t)rows * d * 4;
+    if (to != nullptr && to != from && bytes > 0) {
+        const cudaError_t e = from != nullptr
+                                  ? cudaMemcpyAsync(to, from, bytes, cudaMemcpyDeviceToDevice, s)
+                                  : cudaMemsetAsync(to, 0, bytes, s);
+        if (e != cudaSuccess) return CHOL_ECUDA;
+    }
+    if (status != nullptr && cudaMemsetAsync(status, 0, 4, s) != cudaSuccess) return CHOL_ECUDA;
+    return CHOL_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int chol_rms_norm(int64_t rows, int64_t d, int32_t dtype, int32_t res_dtype, int32_t y_dtype,
+                  int32_t group, float eps, const void* x, int64_t ldx, const void* res,
+                  int64_t ldr, const void* w, void* y, float* scale, void* r, float* rstd,
+                  void* stream) {
+    const size_t es = model_size(dtype), rs = model_size(res_dtype);
+    const bool eight = y_dtype == CHOL_E4M3 || y_dtype == CHOL_I8;
+    if (es == 0 || (res_dtype != dtype && res_dtype != CHOL_F32) || (!eight && y_dtype != dtype))
+        return CHOL_EDTYPE;
+    if (rows < 0 || d <= 0 || d > kMaxD || ldx < 0 || ldr < 0) return CHOL_EINVAL;
+    if (!(eps >= 0.0f) || std::isinf(eps)) return CHOL_EINVAL;
+    if (eight ? (group != 0 && group != 128) : (group != 0 || scale != nullptr))
+        return CHOL_EINVAL;
+    if (rows > 1 && (ldx < d || (res != nullptr && ldr < d))) return CHOL_EINVAL;
+    if ((u128)rows * (u128)std::max(std::max(ldx, ldr), d) * 4 > kMaxBytes) return CHOL_EINVAL;
+    if (rows == 0) return CHOL_OK;
+    if (!usable(x, es) || !usable_or_null(res, rs) || !usable_or_null(w, es) ||
+        !usable(y, eight ? 1 : es) || !usable_or_null(r, rs) || !usable_or_null(rstd, 4) ||
+        (eight && !usable(scale, 4)))
+        return CHOL_EINVAL;
+    const size_t ys = eight ? 1 : es;
+    const u128 groups = group != 0 ? (d + group - 1) / group : 1;
+    if (aliased({{x, span(rows, ldx, d, es), false, nullptr},
+                 {res, span(rows, ldr, d, rs), false, nullptr},
+                 {w, (u128)d * es, false, nullptr},
+                 {y, (u128)rows * d * ys, true, nullptr},
+                 {scale, (u128)rows * groups * 4, true, nullptr},
+                 {r, (u128)rows * d * rs, true, ldr == d ? res : nullptr},
+                 {rstd, (u128)rows * 4, true, nullptr}}))
+        return CHOL_EALIAS;
+    return to_code(chol::rms_norm({rows, d, eps, group, x, ldx, res, ldr, w, y, scale, r, rstd},
+                                  dtype, res_dtype, y_dtype, static_cast<cudaStream_t>(stream)));
+}
+
+int64_t chol_rms_norm_adj_workspace(int64_t rows, int64_t d) {
+    if (rows < 0 || d <= 0 || d > kMaxD) return CHOL_EINVAL;
+    return (int64_t)chol::rms_norm_adj_workspace_bytes(rows, d);
+}
+
+int chol_rms_norm_adj(int64_t rows, int64_t d, int32_t dtype, int32_t r_dtype, const void* adj_y,
+                      int64_t ldy, const void* r, int64_t ldr, const void* w, const float* rstd,
+                      const void* adj_r, void* adj_in, void* adj_x, void* adj_w, void* work,
+                      int64_t work_bytes, void* stream) {
+    const size_t es = model_size(dtype), rs = model_size(r_dtype);
+    if (es == 0 || (r_dtype != dtype && r_dtype != CHOL_F32)) return CHOL_EDTYPE;
+    if (rows < 0 || d <= 0 || d > kMaxD || ldy < 0 || ldr < 0) return CHOL_EINVAL;
+    if (rows > 1 && (ldy < d || ldr < d)) return CHOL_EINVAL;
+    if ((u128)rows * (u128)std::max(std::max(ldy, ldr), d) * 4 > kMaxBytes) return CHOL_EINVAL;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (rows == 0) {  // a sum over no rows
+        if (adj_w == nullptr) return CHOL_OK;
+        if (!usable(adj_w, es)) return CHOL_EINVAL;
+        return to_code(cudaMemsetAsync(adj_w, 0, (size_t)d * es, s));
+    }
+    if (!usable(adj_y, es) || !usable(r, rs) || !usable_or_null(w, es) || !usable(rstd, 4) ||
+        !usable_or_null(adj_r, rs) || !usable_or_null(adj_in, rs) || !usable_or_null(adj_x, es) ||
+        !usable_or_null(adj_w, es) || !work_ok(work, work_bytes))
+        return CHOL_EINVAL;
+    const size_t need = adj_w != nullptr ? chol::rms_norm_adj_workspace_bytes(rows, d) : 0;
+    const u128 n = (u128)rows * d;
+    if (aliased({{adj_y, span(rows, ldy, d, es), false, nullptr},
+                 {r, span(rows, ldr, d, rs), false, nullptr},
+                 {w, (u128)d * es, false, nullptr},
+                 {rstd, (u128)rows * 4, false, nullptr},
+                 {adj_r, n * rs, false, nullptr},
+                 {adj_in, n * rs, true, adj_r},
+                 {adj_x, n * es, true, nullptr},
+                 {adj_w, (u128)d * es, true, nullptr},
+                 {work, need, true, nullptr}}))
+        return CHOL_EALIAS;
+    if (adj_in == nullptr && adj_x == nullptr && adj_w == nullptr) return CHOL_OK;
+    Work scratch(s);
+    void* mem = nullptr;
+    const int rc = scratch.get(work, work_bytes, need, &mem);
+    if (rc != CHOL_OK) return rc;
+    return scratch.done(to_code(chol::rms_norm_adj(
+        {rows, d, adj_y, ldy, r, ldr, w, rstd, adj_r, adj_in, adj_x, adj_w,
+         static_cast<float*>(mem)},
+        dtype, r_dtype, s)));
+}
+
+int64_t chol_linrec_workspace(int64_t batch, int64_t time, int64_t d, int32_t dtype) {
+    if (model_size(dtype) == 0) return CHOL_EDTYPE;
+    if (batch < 0 || time < 0 || d <= 0 || d > kMaxD ||
+        (u128)batch * (u128)time * (u128)d * 4 > kMaxBytes)
+        return CHOL_EINVAL;
+    return (int64_t)chol::linrec_workspace_bytes(batch, time, d, dtype);
+}
+
+int chol_linrec(int64_t batch, int64_t time, int64_t d, int32_t dtype, int32_t gate_kind,
+                int32_t complement, const void* g, int64_t g_bs, int64_t g_ts, const void* x,
+                int64_t x_bs, int64_t x_ts, const float* state0, const int64_t* offsets,
+                int64_t nseq, void* h, float* state1, int32_t* status, void* work,
+                int64_t work_bytes, void* stream) {
+    int rc = check_linrec(batch, time, d, dtype, gate_kind, complement, {g_bs, x_bs}, {g_ts, x_ts},
+                          offsets, nseq);
+    if (rc != CHOL_OK) return rc;
+    if (offsets == nullptr) nseq = batch;
+    if (nseq == 0) return CHOL_OK;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (!usable_or_null(state0, 4) || !usable_or_null(offsets, 8) || !usable_or_null(state1, 4) ||
+        !usable_or_null(status, 4) || !work_ok(work, work_bytes))
+        return CHOL_EINVAL;
+    const size_t es = model_size(dtype);
+    if (time > 0 && (!usable(g, es) || !usable(x, es) || !usable(h, es))) return CHOL_EINVAL;
+    const size_t need = chol::linrec_workspace_bytes(batch, time, d, dtype);
+    const u128 states = (u128)nseq * d * 4;
+    if (aliased({{g, span3(batch, g_bs, time, g_ts, d, es), false, nullptr},
+                 {x, span3(batch, x_bs, time, x_ts, d, es), false, nullptr},
+                 {state0, states, false, nullptr},
+                 {offsets, (u128)(nseq + 1) * 8, false, nullptr},
+                 {h, (u128)batch * time * d * es, true, nullptr},
+                 {state1, states, true, time <= 1 ? state0 : nullptr},
+                 {status, 4, true, nullptr},
+                 {work, need, true, nullptr}}))
+        return CHOL_EALIAS;
+    if (time == 0) return copy_states(state0, state1, nseq, d, status, s);
+    Work scratch(s);
+    void* mem = nullptr;
+    if ((rc = scratch.get(work, work_bytes, need, &mem)) != CHOL_OK) return rc;
+    chol::LinrecArgs a = {};
+    a.batch = batch, a.time = time, a.d = d;
+    a.g = g, a.g_bs = g_bs, a.g_ts = g_ts;
+    a.x = x, a.x_bs = x_bs, a.x_ts = x_ts;
+    a.state0 = state0, a.offsets = offsets, a.nseq = nseq;
+    a.h = h, a.state1 = state1, a.status = status, a.work = mem;
+    return scratch.done(to_code(chol::linrec(a, dtype, gate_kind, complement != 0, false, s)));
+}
+
+int chol_linrec_adj(int64_t batch, int64_t time, int64_t d, int32_t dtype, int32_t gate_kind,
+                    int32_t complement, const void* g, int64_t g_bs, int64_t g_ts, const void* x,
+                    int64_t x_bs, int64_t x_ts, const float* state0, const int64_t* offsets,
+                    int64_t nseq, const void* h, const void* adj_h, int64_t adj_h_bs,
+                    int64_t adj_h_ts, const float* adj_s1, void* adj_g, void* adj_x, float* adj_s0,
+                    int32_t* status, void* work, int64_t work_bytes, void* stream) {
+    const bool has_x = complement != 0;
+    int rc = check_linrec(batch, time, d, dtype, gate_kind, complement,
+                          {g_bs, has_x ? x_bs : 0, adj_h_bs}, {g_ts, has_x ? x_ts : d, adj_h_ts},
+                          offsets, nseq);
+    if (rc != CHOL_OK) return rc;
+    if (offsets == nullptr) nseq = batch;
+    if (nseq == 0) return CHOL_OK;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (!usable_or_null(state0, 4) || !usable_or_null(offsets, 8) || !usable_or_null(adj_s1, 4) ||
+        !usable_or_null(adj_s0, 4) || !usable_or_null(status, 4) || !work_ok(work, work_bytes))
+        return CHOL_EINVAL;
+    const size_t es = model_size(dtype);
+    if (time > 0 && (!usable(g, es) || (has_x && !usable(x, es)) || !usable(h, es) ||
+                     !usable(adj_h, es) || !usable(adj_g, es) || !usable(adj_x, es)))
+        return CHOL_EINVAL;
+    const size_t need = chol::linrec_workspace_bytes(batch, time, d, dtype);
+    const u128 states = (u128)nseq * d * 4, n = (u128)batch * time * d * es;
+    if (aliased({{g, span3(batch, g_bs, time, g_ts, d, es), false, nullptr},
+                 {has_x ? x : nullptr, span3(batch, x_bs, time, x_ts, d, es), false, nullptr},
+                 {state0, states, false, nullptr},
+                 {offsets, (u128)(nseq + 1) * 8, false, nullptr},
+                 {h, n, false, nullptr},
+                 {adj_h, span3(batch, adj_h_bs, time, adj_h_ts, d, es), false, nullptr},
+                 {adj_s1, states, false, nullptr},
+                 {adj_g, n, true, nullptr},
+                 {adj_x, n, true, nullptr},
+                 {adj_s0, states, true, nullptr},
+                 {status, 4, true, nullptr},
+                 {work, need, true, nullptr}}))
+        return CHOL_EALIAS;
+    if (time == 0) return copy_states(adj_s1, adj_s0, nseq, d, status, s);
+    Work scratch(s);
+    void* mem = nullptr;
+    if ((rc = scratch.get(work, work_bytes, need, &mem)) != CHOL_OK) return rc;
+    chol::LinrecArgs a = {};
+    a.batch = batch, a.time = time, a.d = d;
+    a.g = g, a.g_bs = g_bs, a.g_ts = g_ts;
+    a.x = has_x ? x : nullptr, a.x_bs = x_bs, a.x_ts = x_ts;
+    a.state0 = state0, a.offsets = offsets, a.nseq = nseq;
+    a.h = const_cast<void*>(h);
+    a.adj_h = adj_h, a.dh_bs = adj_h_bs, a.dh_ts = adj_h_ts;
+    a.adj_s1 = adj_s1, a.adj_g = adj_g, a.adj_x = adj_x, a.adj_s0 = adj_s0;
+    a.status = status, a.work = mem;
+    return scratch.done(to_code(chol::linrec(a, dtype, gate_kind, complement != 0, true, s)));
+}
+
+int chol_adamw(int64_t count, const chol_adamw_tensor* tensors, int32_t param_dtype,
+               int32_t grad_dtype, int32_t state_bits, double lr, double beta1, double beta2,
+               double eps, int64_t step, const float* grad_scale, const int32_t* status,
+               void* stream) {
+    const bool wide = param_dtype == CHOL_F64;
+    const size_t ps = wide ? 8 : model_size(param_dtype), gs = wide ? 8 : model_size(grad_dtype);
+    if (ps == 0 || gs == 0 || (grad_dtype != param_dtype && param_dtype != CHOL_F32))
+        return CHOL_EDTYPE;
+    if (param_dtype == CHOL_F32 && grad_dtype == CHOL_F64) return CHOL_EDTYPE;
+    if (state_bits != 32 && state_bits != 8) return CHOL_EINVAL;
+    if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !(eps >= 0.0) ||
+        std::isinf(eps) || !std::isfinite(lr) || step < 1 || count < 0)
+        return CHOL_EINVAL;
+    if (count == 0) return CHOL_OK;
+    if (tensors == nullptr || !usable_or_null(grad_scale, 4) || !usable_or_null(status, 4))
+        return CHOL_EINVAL;
+    const bool eight = state_bits == 8;
+    const size_t ss = eight ? 1 : 4;
+    struct Piece {
+        Range r;
+        bool out;
+    };
+    std::vector<Piece> pieces;
+    try {
+        pieces.reserve((size_t)std::min<int64_t>(count, 1 << 24) * 7 + 2);
+        auto add = [&](const void* p, size_t bytes, bool out) {
+            if (p != nullptr) pieces.push_back({range_of(p, bytes), out});
+        };
+        for (int64_t i = 0; i < count; ++i) {
+            const chol_adamw_tensor& t = tensors[i];
+            if (t.numel < 0 || (u128)t.numel * 8 > kMaxBytes || !std::isfinite(t.weight_decay))
+                return CHOL_EINVAL;
+            if (t.numel == 0) continue;
+            if (!usable(t.param, ps) || !usable(t.grad, gs) || !usable(t.m, ss) || !usable(t.v, ss))
+                return CHOL_EINVAL;
+            if (eight ? (!usable(t.m_scale, 4) || !usable(t.v_scale, 4))
+                      : (t.m_scale != nullptr || t.v_scale != nullptr))
+                return CHOL_EINVAL;
+            if (t.copy != nullptr) {
+                if (param_dtype != CHOL_F32 || gs != 2) return CHOL_EDTYPE;
+                if (!usable(t.copy, gs)) return CHOL_EINVAL;
+            }
+            const size_t n = (size_t)t.numel, blocks = (n + 255) / 256;
+            add(t.param, n * ps, true);
+            add(t.grad, n * gs, false);
+            add(t.m, n * ss, true);
+            add(t.v, n * ss, true);
+            add(t.m_scale, blocks * 4, true);
+            add(t.v_scale, blocks * 4, true);
+            add(t.copy, n * gs, true);
+        }
+        add(grad_scale, 4, false);
+        add(status, 4, false);
+        // Sorted by address, an overlap that touches an output is one of a
+        // piece with the furthest-reaching output, or input, before it.
+        std::sort(pieces.begin(), pieces.end(),
+                  [](const Piece& a, const Piece& b) { return a.r.lo < b.r.lo; });
+    } catch (const std::bad_alloc&) {
+        return CHOL_ENOMEM;
+    }
+    uintptr_t out_hi = 0, any_hi = 0;
+    for (const Piece& p : pieces) {
+        if (p.r.lo < out_hi || (p.out && p.r.lo < any_hi)) return CHOL_EALIAS;
+        if (p.out) out_hi = std::max(out_hi, p.r.hi);
+        any_hi = std::max(any_hi, p.r.hi);
+    }
+    return to_code(chol::adamw(count, tensors,
+                               {param_dtype, grad_dtype, state_bits, lr, beta1, beta2, eps, step,
+                                grad_scale, status},
+                               static_cast<cudaStream_t>(stream)));
+}
+
+int32_t chol_learn_version(void) { return CHOL_LEARN_VERSION; }
+
+}  // extern "C"

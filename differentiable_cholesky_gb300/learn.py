@@ -1,0 +1,639 @@
+"""Operators for learning with the factor (declared in ``include/chol_learn.h``):
+what stands before the factor in a model that is trained through it, and the
+optimiser behind its adjoint.
+
+* :func:`rms_norm_fwd`, :func:`rms_norm_quant`, :func:`rms_norm_adj`: the
+  root-mean-square norm with the residual's addition, in the input's type or
+  in 8 bits with scales, and its reverse mode; :func:`rms_norm` for autograd.
+* :func:`linrec_fwd`, :func:`linrec_step`, :func:`linrec_adj`: the gated linear
+  recurrence ``h_t = a_t h_{t-1} + b_t`` over long or packed sequences, one
+  step of it, and its reverse mode; :func:`linrec` for autograd.
+* :class:`AdamW`: a step over many tensors, moments in 32 or in 8 bits.
+
+As in :mod:`.binding`, this is argument marshalling only: every step runs in
+the library's CUDA kernels, and there is no fallback.  Work goes to the
+current stream, or to ``stream``; the caller orders that stream behind what
+made the inputs.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import numpy as np
+import torch
+
+from . import binding as _b
+
+__all__ = ["rms_norm_fwd", "rms_norm_quant", "rms_norm_adj", "rms_norm",
+           "linrec_fwd", "linrec_step", "linrec_adj", "linrec", "AdamW"]
+
+CHOL_F16, CHOL_BF16, CHOL_E4M3, CHOL_I8 = 4, 5, 6, 7
+_MODEL = {torch.float32: _b.CHOL_F32, torch.float16: CHOL_F16, torch.bfloat16: CHOL_BF16}
+_GATES = {"linear": 0, "log": 1, "logit": 2}
+_CODES = {"e4m3": (CHOL_E4M3, torch.float8_e4m3fn), "int8": (CHOL_I8, torch.int8)}
+BLOCK = 256  # moments of AdamW that share a scale
+
+_lib = None
+
+
+def _library():
+    global _lib
+    if _lib is None:
+        lib = _b.load_library()
+        i64, i32, f32, f64, vp = (ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_double,
+                                  ctypes.c_void_p)
+        lib.chol_rms_norm.argtypes = [i64, i64, i32, i32, i32, i32, f32, vp, i64, vp, i64, vp, vp,
+                                      vp, vp, vp, vp]
+        lib.chol_rms_norm_adj.argtypes = [i64, i64, i32, i32, vp, i64, vp, i64, vp, vp, vp, vp, vp,
+                                          vp, vp, i64, vp]
+        lib.chol_rms_norm_adj_workspace.argtypes = [i64, i64]
+        lib.chol_linrec.argtypes = [i64, i64, i64, i32, i32, i32, vp, i64, i64, vp, i64, i64, vp,
+                                    vp, i64, vp, vp, vp, vp, i64, vp]
+        lib.chol_linrec_adj.argtypes = [i64, i64, i64, i32, i32, i32, vp, i64, i64, vp, i64, i64,
+                                        vp, vp, i64, vp, vp, i64, i64, vp, vp, vp, vp, vp, vp,
+                                        i64, vp]
+        lib.chol_linrec_workspace.argtypes = [i64, i64, i64, i32]
+        lib.chol_adamw.argtypes = [i64, vp, i32, i32, i32, f64, f64, f64, f64, i64, vp, vp, vp]
+        for f in (lib.chol_rms_norm, lib.chol_rms_norm_adj, lib.chol_linrec, lib.chol_linrec_adj,
+                  lib.chol_adamw):
+            f.restype = ctypes.c_int
+        for f in (lib.chol_rms_norm_adj_workspace, lib.chol_linrec_workspace):
+            f.restype = i64
+        lib.chol_learn_version.argtypes = []
+        lib.chol_learn_version.restype = i32
+        _lib = lib
+    return _lib
+
+
+def _check(rc: int):
+    if rc != 0:
+        _b._check(rc)
+
+
+def _ptr(x):
+    return None if x is None else x.data_ptr()
+
+
+def _on(stream, inputs, call):
+    """``call()`` with ``stream`` as the current one: what it allocates belongs
+    to that stream, and the inputs' memory is not given to others before its
+    work is done."""
+    if stream is None:
+        return call()
+    with torch.cuda.stream(stream):
+        out = call()
+    for x in inputs:
+        if x is not None:
+            x.record_stream(stream)
+    return out
+
+
+def _model(x, name: str, like: torch.Tensor | None = None):
+    """Checks a CUDA tensor of a model type (of `like`'s type and device)."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if x.dtype not in _MODEL:
+        raise ValueError(f"{name}: unsupported dtype {x.dtype}")
+    if like is not None and (x.dtype != like.dtype or x.device != like.device):
+        raise ValueError(f"{name} must have dtype {like.dtype} on {like.device}, "
+                         f"got {x.dtype} on {x.device}")
+
+
+def _f32(x, name: str, shape, like: torch.Tensor):
+    """Checks a contiguous float32 tensor of a shape (None passes)."""
+    if x is None:
+        return
+    if not isinstance(x, torch.Tensor) or x.device != like.device:
+        raise ValueError(f"{name} must be a tensor on {like.device}")
+    if x.dtype != torch.float32 or tuple(x.shape) != tuple(shape) or not x.is_contiguous():
+        raise ValueError(f"{name} must be contiguous float32 {tuple(shape)}, "
+                         f"got {x.dtype} {tuple(x.shape)}")
+
+
+def _rows(x: torch.Tensor, name: str):
+    """(rows, d, row stride) of ``[..., d]``: contiguous, or rows of
+    contiguous elements at one stride."""
+    if x.dim() < 1:
+        raise ValueError(f"{name} must have at least one dimension")
+    d = x.shape[-1]
+    if x.is_contiguous():
+        return (x.numel() // d if d else 0), d, d
+    ok = x.stride(-1) == 1 or d == 1
+    ld, rows = d, 1
+    for i in range(x.dim() - 2, -1, -1):
+        if x.shape[i] == 1:
+            continue
+        if rows == 1:
+            ld = x.stride(i)
+        elif x.stride(i) != ld * rows:
+            ok = False
+        rows *= x.shape[i]
+    if not ok or ld < d:
+        raise ValueError(f"{name} must have contiguous rows at one stride, got strides {x.stride()}")
+    return rows, d, ld
+
+
+def _same_shape(x, y, names):
+    if tuple(x.shape) != tuple(y.shape):
+        raise ValueError(f"{names[0]} must match {names[1]}'s shape {tuple(y.shape)}, "
+                         f"got {tuple(x.shape)}")
+
+
+# ----------------------------------------------------------------------------
+# Root-mean-square norm
+# ----------------------------------------------------------------------------
+def _rms_forward(x, weight, residual, eps, code, group, stream):
+    _model(x, "x")
+    rows, d, ldx = _rows(x, "x")
+    if d == 0:
+        raise ValueError("x must have at least one column")
+    if weight is not None:
+        _model(weight, "weight", x)
+        if tuple(weight.shape) != (d,) or not weight.is_contiguous():
+            raise ValueError(f"weight must be contiguous [{d}], got {tuple(weight.shape)}")
+    ldr, rtype = d, x.dtype
+    if residual is not None:
+        _model(residual, "residual")
+        _same_shape(residual, x, ("residual", "x"))
+        if residual.device != x.device:
+            raise ValueError(f"residual must be on {x.device}")
+        rtype = residual.dtype
+        if rtype != x.dtype and rtype != torch.float32:
+            raise ValueError(f"residual must have dtype {x.dtype} or float32, got {rtype}")
+        ldr = _rows(residual, "residual")[2]
+
+    def call():
+        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        r = torch.empty(x.shape, dtype=rtype, device=x.device) if residual is not None else None
+        scale = None
+        if code is None:
+            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            ytype = _MODEL[x.dtype]
+        else:
+            ytype = code[0]
+            y = torch.empty(x.shape, dtype=code[1], device=x.device)
+            groups = -(-d // group) if group else 1
+            scale = torch.empty(x.shape[:-1] + (groups,), dtype=torch.float32, device=x.device)
+        _check(_library().chol_rms_norm(
+            rows, d, _MODEL[x.dtype], _MODEL[rtype], ytype, group, eps, x.data_ptr(), ldx,
+            _ptr(residual), ldr, _ptr(weight), y.data_ptr(), _ptr(scale), _ptr(r),
+            rstd.data_ptr(), _b._stream_ptr(stream)))
+        return y, scale, x if r is None else r, rstd
+
+    return _on(stream, (x, weight, residual), call)
+
+
+def rms_norm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None,
+                 residual: torch.Tensor | None = None, eps: float = 1e-6, stream=None):
+    """``y, r, rstd`` with ``r = x + residual``, ``rstd = 1 / sqrt(mean(r^2) + eps)``
+    over the last dimension and ``y = r * rstd * weight``.
+
+    ``x`` is ``[..., d]`` in float32, float16 or bfloat16 (a slice of wider rows
+    is fine), ``weight`` ``[d]`` of the same type, ``residual`` of ``x``'s shape
+    in its type or in float32.  ``r`` has the residual's type and is ``x``
+    itself without one; ``rstd`` is float32 ``[...]``."""
+    y, _, r, rstd = _rms_forward(x, weight, residual, eps, None, 0, stream)
+    return y, r, rstd
+
+
+def rms_norm_quant(x: torch.Tensor, weight: torch.Tensor | None = None,
+                   residual: torch.Tensor | None = None, eps: float = 1e-6, kind: str = "e4m3",
+                   group: int = 0, stream=None):
+    """``q, scale, r, rstd``: as :func:`rms_norm_fwd` with ``y`` in 8 bits
+    (``kind`` "e4m3" or "int8"), ``y ~ q * scale``.  One scale for each row
+    (``group`` 0; ``scale`` is ``[..., 1]``) or for each 128 columns (``group``
+    128; ``[..., ceil(d / 128)]``)."""
+    if kind not in _CODES:
+        raise ValueError(f"unknown kind {kind!r}; expected one of {sorted(_CODES)}")
+    if group not in (0, 128):
+        raise ValueError(f"group must be 0 or 128, got {group}")
+    return _rms_forward(x, weight, residual, eps, _CODES[kind], group, stream)
+
+
+def rms_norm_adj(adj_y: torch.Tensor, r: torch.Tensor, rstd: torch.Tensor,
+                 weight: torch.Tensor | None = None, adj_r: torch.Tensor | None = None,
+                 want_weight: bool = True, stream=None):
+    """Reverse mode of :func:`rms_norm_fwd`: ``adj_in, adj_weight`` for the
+    gradient ``adj_y`` of ``y`` and, where something else reads ``r``, ``adj_r``
+    of it.  ``adj_in`` (in ``r``'s type) is the gradient of the residual and of
+    ``x`` alike; ``adj_weight`` is None without a weight or ``want_weight``."""
+    _model(adj_y, "adj_y")
+    _model(r, "r")
+    _same_shape(r, adj_y, ("r", "adj_y"))
+    if r.device != adj_y.device or (r.dtype != adj_y.dtype and r.dtype != torch.float32):
+        raise ValueError(f"r must have dtype {adj_y.dtype} or float32 on {adj_y.device}, "
+                         f"got {r.dtype} on {r.device}")
+    rows, d, ldy = _rows(adj_y, "adj_y")
+    if d == 0:
+        raise ValueError("adj_y must have at least one column")
+    ldr = _rows(r, "r")[2]
+    _f32(rstd, "rstd", adj_y.shape[:-1], adj_y)
+    if rstd is None:
+        raise ValueError("rstd is needed")
+    if weight is not None:
+        _model(weight, "weight", adj_y)
+        if tuple(weight.shape) != (d,) or not weight.is_contiguous():
+            raise ValueError(f"weight must be contiguous [{d}], got {tuple(weight.shape)}")
+    if adj_r is not None:
+        _model(adj_r, "adj_r", r)
+        _same_shape(adj_r, adj_y, ("adj_r", "adj_y"))
+        if not adj_r.is_contiguous():
+            raise ValueError("adj_r must be contiguous")
+    want_weight = want_weight and weight is not None
+
+    def call():
+        lib = _library()
+        adj_in = torch.empty(r.shape, dtype=r.dtype, device=r.device)
+        adj_w = work = None
+        need = 0
+        if want_weight:
+            adj_w = torch.empty_like(weight)
+            need = lib.chol_rms_norm_adj_workspace(rows, d)
+            work = torch.empty(need, dtype=torch.uint8, device=r.device)
+        _check(lib.chol_rms_norm_adj(
+            rows, d, _MODEL[adj_y.dtype], _MODEL[r.dtype], adj_y.data_ptr(), ldy, r.data_ptr(),
+            ldr, _ptr(weight), rstd.data_ptr(), _ptr(adj_r), adj_in.data_ptr(), None, _ptr(adj_w),
+            _ptr(work) if need else None, need, _b._stream_ptr(stream)))
+        return adj_in, adj_w
+
+    return _on(stream, (adj_y, r, rstd, weight, adj_r), call)
+
+
+class _RmsNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps):
+        y, r, rstd = rms_norm_fwd(x, weight, residual, eps)
+        ctx.save_for_backward(r, rstd, weight)
+        ctx.types = (x.dtype, residual is not None)
+        if residual is None:
+            r = x.new_empty(0)
+            ctx.mark_non_differentiable(r)
+        return y, r
+
+    @staticmethod
+    def backward(ctx, adj_y, adj_r):
+        r, rstd, weight = ctx.saved_tensors
+        xtype, has_res = ctx.types
+        adj_in, adj_w = rms_norm_adj(adj_y.contiguous(), r, rstd, weight,
+                                     adj_r=adj_r.contiguous() if has_res else None,
+                                     want_weight=ctx.needs_input_grad[1])
+        return adj_in.to(xtype), adj_w, adj_in if has_res else None, None
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
+             residual: torch.Tensor | None = None, eps: float = 1e-6):
+    """Differentiable norm: ``y``, or ``(y, r)`` with a residual."""
+    y, r = _RmsNorm.apply(x, weight, residual, eps)
+    return y if residual is None else (y, r)
+
+
+# ----------------------------------------------------------------------------
+# Gated linear recurrence
+# ----------------------------------------------------------------------------
+def _sequence(x, name: str, packed: bool, like=None):
+    """(batch, time, d, batch stride, time stride) of ``[B, T, D]`` or ``[T, D]``."""
+    _model(x, name, like)
+    if x.dim() not in ((2,) if packed else (2, 3)):
+        raise ValueError(f"{name} must be [T, D]{'' if packed else ' or [B, T, D]'}, "
+                         f"got {tuple(x.shape)}")
+    if like is not None:
+        _same_shape(x, like, (name, "x"))
+    batch, (time, d) = (x.shape[0] if x.dim() == 3 else 1), x.shape[-2:]
+    ts, bs = x.stride(-2), (x.stride(0) if x.dim() == 3 else 0)
+    if d == 0:
+        raise ValueError(f"{name} must have at least one channel")
+    if (x.stride(-1) != 1 and d > 1) or (ts < d and time > 1):
+        raise ValueError(f"{name} must have contiguous channels, got strides {x.stride()}")
+    return batch, time, d, bs, ts
+
+
+def _recurrence(gate, x, state, offsets, kind):
+    if kind not in _GATES:
+        raise ValueError(f"unknown kind {kind!r}; expected one of {sorted(_GATES)}")
+    packed = offsets is not None
+    shape = _sequence(x, "x", packed)
+    strides = _sequence(gate, "gate", packed, x)[3:]
+    n = shape[0]
+    if packed:
+        if (not isinstance(offsets, torch.Tensor) or offsets.device != x.device
+                or offsets.dtype != torch.int64 or offsets.dim() != 1 or offsets.numel() < 1
+                or not offsets.is_contiguous()):
+            raise ValueError(f"offsets must be a contiguous int64 vector on {x.device}")
+        n = offsets.numel() - 1
+    _f32(state, "state", (n, shape[2]), x)
+    return shape, strides, n
+
+
+def _work(lib, shape, x):
+    need = lib.chol_linrec_workspace(shape[0], shape[1], shape[2], _MODEL[x.dtype])
+    if need <= 0:
+        return None, 0
+    return torch.empty(need, dtype=torch.uint8, device=x.device), need
+
+
+def linrec_fwd(gate: torch.Tensor, x: torch.Tensor, state: torch.Tensor | None = None,
+               offsets: torch.Tensor | None = None, kind: str = "logit", complement: bool = True,
+               stream=None):
+    """``h, state`` of ``h_t = a_t h_{t-1} + b_t`` along ``T`` of ``[B, T, D]`` (or
+    ``[T, D]``), every channel by itself.
+
+    ``a`` is ``gate`` ("linear"), ``exp(gate)`` ("log") or ``sigmoid(gate)``
+    ("logit"); ``b`` is ``(1 - a) x`` with ``complement``, else ``x``.  With
+    ``offsets`` (int64 ``[S + 1]``, from 0 to ``T``) the rows of ``[T, D]`` are
+    ``S`` sequences one behind another, of any lengths, also none.  ``state``
+    (float32 ``[B or S, D]``) is what each begins with, zeros by default; the
+    returned one is what each ends with, not rounded to ``x``'s type."""
+    shape, (gbs, gts), n = _recurrence(gate, x, state, offsets, kind)
+    batch, time, d, bs, ts = shape
+
+    def call():
+        lib = _library()
+        h = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        last = torch.empty((n, d), dtype=torch.float32, device=x.device)
+        work, need = _work(lib, shape, x)
+        _check(lib.chol_linrec(
+            batch, time, d, _MODEL[x.dtype], _GATES[kind], int(complement), gate.data_ptr(), gbs,
+            gts, x.data_ptr(), bs, ts, _ptr(state), _ptr(offsets), n, h.data_ptr(),
+            last.data_ptr(), None, _ptr(work), need, _b._stream_ptr(stream)))
+        return h, last
+
+    return _on(stream, (gate, x, state, offsets), call)
+
+
+def linrec_step(gate: torch.Tensor, x: torch.Tensor, state: torch.Tensor, kind: str = "logit",
+                complement: bool = True, stream=None):
+    """One step for ``[B, D]`` gates and values: updates ``state`` (float32
+    ``[B, D]``) in place and returns ``h`` ``[B, D]`` in ``x``'s type."""
+    if kind not in _GATES:
+        raise ValueError(f"unknown kind {kind!r}; expected one of {sorted(_GATES)}")
+    _model(x, "x")
+    _model(gate, "gate", x)
+    _same_shape(gate, x, ("gate", "x"))
+    if x.dim() != 2 or x.shape[1] == 0:
+        raise ValueError(f"x must be [B, D], got {tuple(x.shape)}")
+    batch, d = x.shape
+    for name, t in (("x", x), ("gate", gate)):
+        if (t.stride(1) != 1 and d > 1) or (t.stride(0) < d and batch > 1):
+            raise ValueError(f"{name} must have contiguous channels, got strides {t.stride()}")
+    if state is None:
+        raise ValueError("state is needed")
+    _f32(state, "state", (batch, d), x)
+
+    def call():
+        h = torch.empty((batch, d), dtype=x.dtype, device=x.device)
+        _check(_library().chol_linrec(
+            batch, 1, d, _MODEL[x.dtype], _GATES[kind], int(complement), gate.data_ptr(),
+            gate.stride(0), d, x.data_ptr(), x.stride(0), d, state.data_ptr(), None, batch,
+            h.data_ptr(), state.data_ptr(), None, None, 0, _b._stream_ptr(stream)))
+        return h
+
+    return _on(stream, (gate, x, state), call)
+
+
+def linrec_adj(gate: torch.Tensor, x: torch.Tensor, h: torch.Tensor, adj_h: torch.Tensor,
+               state: torch.Tensor | None = None, adj_state: torch.Tensor | None = None,
+               offsets: torch.Tensor | None = None, kind: str = "logit", complement: bool = True,
+               stream=None):
+    """Reverse mode of :func:`linrec_fwd`: ``adj_gate, adj_x, adj_state0`` for
+    gradients ``adj_h`` of ``h`` and ``adj_state`` of the final states (zeros by
+    default).  ``h`` is the forward's output; ``adj_state0`` is the gradient of
+    the initial states."""
+    shape, (gbs, gts), n = _recurrence(gate, x, state, offsets, kind)
+    batch, time, d, bs, ts = shape
+    dbs, dts = _sequence(adj_h, "adj_h", offsets is not None, x)[3:]
+    _model(h, "h", x)
+    _same_shape(h, x, ("h", "x"))
+    if not h.is_contiguous():
+        raise ValueError("h must be contiguous")
+    _f32(adj_state, "adj_state", (n, d), x)
+
+    def call():
+        lib = _library()
+        adj_g = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        adj_x = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        adj_0 = torch.empty((n, d), dtype=torch.float32, device=x.device)
+        work, need = _work(lib, shape, x)
+        _check(lib.chol_linrec_adj(
+            batch, time, d, _MODEL[x.dtype], _GATES[kind], int(complement), gate.data_ptr(), gbs,
+            gts, x.data_ptr(), bs, ts, _ptr(state), _ptr(offsets), n, h.data_ptr(),
+            adj_h.data_ptr(), dbs, dts, _ptr(adj_state), adj_g.data_ptr(), adj_x.data_ptr(),
+            adj_0.data_ptr(), None, _ptr(work), need, _b._stream_ptr(stream)))
+        return adj_g, adj_x, adj_0
+
+    return _on(stream, (gate, x, h, adj_h, state, adj_state, offsets), call)
+
+
+class _Linrec(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, gate, x, state, offsets, kind, complement):
+        h, last = linrec_fwd(gate, x, state, offsets, kind, complement)
+        ctx.save_for_backward(gate, x, h, state, offsets)
+        ctx.how = (kind, complement)
+        ctx.set_materialize_grads(False)
+        return h, last
+
+    @staticmethod
+    def backward(ctx, adj_h, adj_last):
+        gate, x, h, state, offsets = ctx.saved_tensors
+        if adj_h is None and adj_last is None:
+            return (None,) * 6
+        adj_h = torch.zeros_like(h) if adj_h is None else adj_h.contiguous()
+        adj_last = None if adj_last is None else adj_last.contiguous()
+        adj_g, adj_x, adj_0 = linrec_adj(gate, x, h, adj_h, state, adj_last, offsets, *ctx.how)
+        return adj_g, adj_x, None if state is None else adj_0, None, None, None
+
+
+def linrec(gate: torch.Tensor, x: torch.Tensor, state: torch.Tensor | None = None,
+           offsets: torch.Tensor | None = None, kind: str = "logit", complement: bool = True):
+    """Differentiable ``(h, state)`` of :func:`linrec_fwd`."""
+    return _Linrec.apply(gate, x, state, offsets, kind, complement)
+
+
+# ----------------------------------------------------------------------------
+# AdamW
+# ----------------------------------------------------------------------------
+_ENTRY = np.dtype([("numel", "i8"), ("param", "u8"), ("grad", "u8"), ("m", "u8"), ("v", "u8"),
+                   ("m_scale", "u8"), ("v_scale", "u8"), ("copy", "u8"), ("weight_decay", "f8")])
+_PARAM = {**_MODEL, torch.float64: _b.CHOL_F64}
+#: gradient types that a parameter type takes
+_GRADS = {torch.float32: (torch.float32, torch.bfloat16, torch.float16),
+          torch.float16: (torch.float16,), torch.bfloat16: (torch.bfloat16,),
+          torch.float64: (torch.float64,)}
+
+
+class AdamW:
+    """AdamW over a list of tensors (float32, float16, bfloat16 or float64,
+    contiguous), all of them updated by one launch for each pair of parameter
+    and gradient types.
+
+    ``weight_decay`` is one number, or one for each tensor.  ``state_bits`` 32
+    keeps the moments in float32; 8 keeps ``m`` and ``sqrt(v)`` as E4M3 values
+    with a float32 scale for every 256 consecutive elements.  ``copies`` (a
+    list with a tensor or None for each parameter) receives float32 parameters
+    rounded to the gradients' 16-bit type.  ``state`` (as from
+    :meth:`state_dict`) adopts moments instead of starting from zeros: its
+    tensors are updated in place.
+
+    :attr:`m`, :attr:`v` (and :attr:`m_scale`, :attr:`v_scale`) are the
+    moments, one tensor for each parameter."""
+
+    def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
+                 weight_decay=1e-2, state_bits: int = 32, copies=None, state=None):
+        self.params = list(params)
+        if state_bits not in (32, 8):
+            raise ValueError(f"state_bits must be 32 or 8, got {state_bits}")
+        n = len(self.params)
+        decay = [float(w) for w in weight_decay] if isinstance(weight_decay, (list, tuple)) \
+            else [float(weight_decay)] * n
+        if len(decay) != n:
+            raise ValueError("weight_decay must be a number, or one for each parameter")
+        self.lr, self.betas, self.eps, self.state_bits = float(lr), tuple(betas), float(eps), state_bits
+        self.steps = 0
+        self.copies = [None] * n if copies is None else list(copies)
+        if len(self.copies) != n:
+            raise ValueError("copies must have an entry for each parameter")
+        for i, p in enumerate(self.params):
+            if not isinstance(p, torch.Tensor) or not p.is_cuda or p.dtype not in _PARAM:
+                raise ValueError(f"parameter {i} must be a CUDA tensor of a floating type of 16 "
+                                 "bits or more")
+            if not p.is_contiguous() or p.device != self.params[0].device:
+                raise ValueError(f"parameter {i} must be contiguous, on the first one's device")
+            c = self.copies[i]
+            if c is not None and (p.dtype != torch.float32 or c.device != p.device
+                                  or c.dtype not in (torch.bfloat16, torch.float16)
+                                  or c.shape != p.shape or not c.is_contiguous()):
+                raise ValueError(f"copy {i} must be a contiguous 16-bit tensor like its float32 "
+                                 "parameter")
+        self._adopt(self._new_state() if state is None else state)
+        self._table = np.zeros(n, _ENTRY)
+        t = self._table
+        t["numel"] = [p.numel() for p in self.params]
+        t["weight_decay"] = decay
+
+    def _new_state(self):
+        """Zero moments: one allocation for each kind, tensors from 256 to 256."""
+        sizes = [-(-p.numel() // BLOCK) * BLOCK for p in self.params]
+        dev = self.params[0].device if self.params else "cuda"
+        kind = torch.float32 if self.state_bits == 32 else torch.uint8
+
+        def views(total, dtype, lengths, shapes):
+            flat, at, out = torch.zeros(total, dtype=dtype, device=dev), 0, []
+            for length, shape in zip(lengths, shapes):
+                count = int(np.prod(shape, dtype=np.int64))
+                out.append(flat[at:at + count].view(shape))
+                at += length
+            return out
+
+        shapes = [tuple(p.shape) for p in self.params]
+        state = {"step": 0}
+        for name in ("m", "v"):
+            got = views(sum(sizes), kind, sizes, shapes)
+            state[name] = [x.view(torch.float8_e4m3fn) for x in got] if self.state_bits == 8 else got
+            if self.state_bits == 8:
+                blocks = [s // BLOCK for s in sizes]
+                state[name + "_scale"] = views(sum(blocks), torch.float32, blocks,
+                                               [(b,) for b in blocks])
+        return state
+
+    def _adopt(self, state):
+        eight = self.state_bits == 8
+        kind = torch.float8_e4m3fn if eight else torch.float32
+        got = {}
+        for name in ("m", "v") + (("m_scale", "v_scale") if eight else ()):
+            xs = list(state[name])
+            if len(xs) != len(self.params):
+                raise ValueError(f"state {name} must have a tensor for each parameter")
+            for i, (x, p) in enumerate(zip(xs, self.params)):
+                count, want = p.numel(), kind
+                if name.endswith("scale"):
+                    count, want = -(-count // BLOCK), torch.float32
+                if x.dtype != want or x.device != p.device or x.numel() != count \
+                        or not x.is_contiguous():
+                    raise ValueError(f"state {name}[{i}] must be contiguous {want} with {count} "
+                                     "elements")
+            got[name] = xs
+        step = int(state["step"])
+        if step < 0:
+            raise ValueError("state step must not be negative")
+        self.steps = step
+        self.m, self.v = got["m"], got["v"]
+        self.m_scale, self.v_scale = got.get("m_scale"), got.get("v_scale")
+
+    def state_dict(self):
+        """The step count and the moments (the tensors themselves)."""
+        out = {"step": self.steps, "m": list(self.m), "v": list(self.v)}
+        if self.state_bits == 8:
+            out.update(m_scale=list(self.m_scale), v_scale=list(self.v_scale))
+        return out
+
+    def load_state_dict(self, state):
+        """Copies a state (as from :meth:`state_dict`) into this one's tensors."""
+        for name, own in (("m", self.m), ("v", self.v), ("m_scale", self.m_scale),
+                          ("v_scale", self.v_scale)):
+            if own is None:
+                continue
+            if len(state[name]) != len(own):
+                raise ValueError(f"state {name} must have a tensor for each parameter")
+            for x, y in zip(own, state[name]):
+                if x.dtype != y.dtype or x.numel() != y.numel():
+                    raise ValueError(f"state {name} does not match the parameters")
+                raw = torch.uint8 if x.dtype == torch.float8_e4m3fn else x.dtype
+                x.view(raw).view(-1).copy_(y.detach().view(raw).reshape(-1))
+        self.steps = int(state["step"])
+
+    def step(self, grads=None, lr: float | None = None, grad_scale: torch.Tensor | None = None,
+             status: torch.Tensor | None = None, stream=None):
+        """One step with ``grads`` (a list with a tensor or None for each
+        parameter; their ``.grad`` by default; parameters without one stay as
+        they are).  ``grad_scale`` is a float32 CUDA scalar that multiplies
+        every gradient (a clipping factor, or one over the loss's scale);
+        ``status`` an int32 one: where it is not 0 on the device nothing is
+        written (the step is still counted)."""
+        grads = [p.grad for p in self.params] if grads is None else list(grads)
+        if len(grads) != len(self.params):
+            raise ValueError("grads must have an entry for each parameter")
+        dev = self.params[0].device if self.params else None
+        for name, x, kind in (("grad_scale", grad_scale, torch.float32),
+                              ("status", status, torch.int32)):
+            if x is not None and (x.dtype != kind or x.numel() != 1 or x.device != dev):
+                raise ValueError(f"{name} must be one {kind} value on {dev}")
+        calls = {}
+        for i, (p, g) in enumerate(zip(self.params, grads)):
+            if g is None:
+                continue
+            if g.dtype not in _GRADS[p.dtype] or g.device != dev or g.numel() != p.numel() \
+                    or not g.is_contiguous():
+                raise ValueError(f"gradient {i} must be contiguous with its parameter's shape, of "
+                                 f"a type in {_GRADS[p.dtype]}, got {g.dtype} {tuple(g.shape)}")
+            c = self.copies[i]
+            if c is not None and c.dtype != g.dtype:
+                raise ValueError(f"copy {i} must have its gradient's dtype {g.dtype}")
+            calls.setdefault((p.dtype, g.dtype), []).append(i)
+        lr = self.lr if lr is None else float(lr)
+
+        def call():
+            for (pt, gt), at in calls.items():
+                whole = len(at) == len(self.params)
+                t = self._table.copy() if whole else self._table[at]
+                pick = (lambda xs: xs) if whole else (lambda xs: [xs[i] for i in at])
+                t["param"] = [x.data_ptr() for x in pick(self.params)]
+                t["grad"] = [x.data_ptr() for x in pick(grads)]
+                t["m"] = [x.data_ptr() for x in pick(self.m)]
+                t["v"] = [x.data_ptr() for x in pick(self.v)]
+                if self.state_bits == 8:
+                    t["m_scale"] = [x.data_ptr() for x in pick(self.m_scale)]
+                    t["v_scale"] = [x.data_ptr() for x in pick(self.v_scale)]
+                t["copy"] = [0 if x is None else x.data_ptr() for x in pick(self.copies)]
+                _check(_library().chol_adamw(
+                    len(at), t.ctypes.data, _PARAM[pt], _PARAM[gt], self.state_bits, lr,
+                    self.betas[0], self.betas[1], self.eps, self.steps + 1, _ptr(grad_scale),
+                    _ptr(status), _b._stream_ptr(stream)))
+
+        used = [grad_scale, status]
+        if stream is not None:
+            for xs in (self.params, grads, self.copies, self.m, self.v, self.m_scale, self.v_scale):
+                used += [xs[i] for at in calls.values() for i in at] if xs is not None else []
+        _on(stream, used, call)
+        self.steps += 1
+        for at in calls.values():
+            torch.autograd.graph.increment_version([self.params[i] for i in at])

@@ -1,0 +1,205 @@
+/*
+ * chol_learn.h -- operators for learning with the factor (chol.h): what stands
+ * before the factor in a model that is trained through it, and the optimiser
+ * behind its adjoint.
+ *
+ *   chol_rms_norm    r = x + res, y = r w / sqrt(mean(r^2) + eps) over rows,
+ *                    y in the input's type or in 8 bits with scales;
+ *                    chol_rms_norm_adj is its reverse mode.
+ *   chol_linrec      the gated linear recurrence h_t = a_t h_{t-1} + b_t, one
+ *                    channel beside another: forward substitution with a
+ *                    bidiagonal factor, without the dense factor;
+ *                    chol_linrec_adj is its reverse mode.
+ *   chol_adamw       one AdamW step over many tensors, moments in 32 or 8 bits.
+ *
+ * The conventions are chol.h's: device pointers owned by the caller, work only
+ * enqueued on `stream`, negative return codes (chol_strerror) for invalid
+ * arguments with nothing enqueued, sizes of zero as no-ops.  Sums, states and
+ * moments are held in float32 whatever the element type; results are rounded
+ * once, to nearest even, when they are written.  The outputs of one call are
+ * the same bits each time.
+ */
+#ifndef CHOL_LEARN_GB300_H
+#define CHOL_LEARN_GB300_H
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "chol.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Element types of these operators beside CHOL_F32 and CHOL_F64. */
+enum {
+    CHOL_F16 = 4,
+    CHOL_BF16 = 5,
+    CHOL_E4M3 = 6, /* 8-bit float, 4 exponent and 3 mantissa bits, largest value 448, no infinities */
+    CHOL_I8 = 7    /* signed 8-bit integer, used from -127 to 127 */
+};
+
+/* Gates of the recurrence. */
+enum {
+    CHOL_GATE_LINEAR = 0, /* a = g                                        */
+    CHOL_GATE_LOG = 1,    /* a = exp(g): g is the logarithm of the decay  */
+    CHOL_GATE_LOGIT = 2   /* a = 1 / (1 + exp(-g))                        */
+};
+
+/*
+ * chol_rms_norm -- for each of `rows` rows of d columns:
+ *     r = x + res (r = x without res),   rstd = 1 / sqrt(sum(r^2) / d + eps),
+ *     y = r * rstd * w (w = 1 without w).
+ *   dtype      CHOL_F32, CHOL_F16 or CHOL_BF16: the type of x and w.
+ *   res_dtype  the type of res and r: dtype or CHOL_F32.
+ *   y_dtype    dtype, or CHOL_E4M3 / CHOL_I8 for 8-bit output with scales.
+ *   group      8-bit output: 0 for one scale per row, or 128 for one per 128
+ *              columns (the last group of a row may be shorter).  Else 0.
+ *   x       in : rows of d elements, row i at x + i * ldx elements (ldx >= d).
+ *   res     in : (or NULL) rows likewise, at stride ldr.
+ *   w       in : (or NULL) d elements.
+ *   y       out: y_dtype[rows][d].  Computed from r before r is rounded.
+ *   scale   out: float[rows][groups] (8-bit output only, else NULL): the
+ *                largest |y| of the group over 448 (E4M3) or 127 (I8);
+ *                y stands for q * scale, q rounded to nearest even.  A group
+ *                of zeros (or of values so small that its scale would be
+ *                below 2^-126) has scale 0 and q 0; one that holds a NaN or an
+ *                infinity has that as its scale, and its q are unspecified.
+ *   r       out: (or NULL) res_dtype[rows][d].  May be res itself where
+ *                ldr == d.
+ *   rstd    out: (or NULL) float[rows], for chol_rms_norm_adj.
+ * Other overlaps of an output with an input or output return CHOL_EALIAS.
+ * eps >= 0; a row of zeros with eps = 0 gives NaN, by the formula.
+ */
+CHOL_API int chol_rms_norm(int64_t rows, int64_t d, int32_t dtype, int32_t res_dtype,
+                           int32_t y_dtype, int32_t group, float eps, const void* x, int64_t ldx,
+                           const void* res, int64_t ldr, const void* w, void* y, float* scale,
+                           void* r, float* rstd, void* stream);
+
+/*
+ * chol_rms_norm_adj -- reverse mode.  With n = r * rstd and u = adj_y * w:
+ *     adj_in = rstd * (u - n * mean(u * n)) + adj_r,   adj_w = sum over rows of adj_y * n.
+ *   dtype      the type of adj_y, w, adj_x and adj_w;  r_dtype that of r,
+ *              adj_r and adj_in (dtype or CHOL_F32).
+ *   adj_y   in : rows at stride ldy.      r  in : rows at stride ldr (x itself
+ *                where the forward had no residual).
+ *   w       in : (or NULL).               rstd in: float[rows].
+ *   adj_r   in : (or NULL) r_dtype[rows][d], the gradient of r from what else
+ *                reads it.
+ *   adj_in  out: (or NULL) r_dtype[rows][d]: the gradient of res, and of x.
+ *                May be adj_r itself.
+ *   adj_x   out: (or NULL) dtype[rows][d]: the same rounded to x's type.
+ *   adj_w   out: (or NULL) dtype[d].
+ *   work       device memory of at least chol_rms_norm_adj_workspace() bytes,
+ *              16-byte aligned, or NULL: then it is taken with cudaMallocAsync
+ *              on `stream` (CHOL_ENOMEM on failure).
+ */
+CHOL_API int chol_rms_norm_adj(int64_t rows, int64_t d, int32_t dtype, int32_t r_dtype,
+                               const void* adj_y, int64_t ldy, const void* r, int64_t ldr,
+                               const void* w, const float* rstd, const void* adj_r, void* adj_in,
+                               void* adj_x, void* adj_w, void* work, int64_t work_bytes,
+                               void* stream);
+CHOL_API int64_t chol_rms_norm_adj_workspace(int64_t rows, int64_t d);
+
+/*
+ * chol_linrec -- h_t = a_t * h_{t-1} + b_t, for `batch` rows of `time` steps of
+ * d channels.  a comes from the gate g by `gate_kind`; b = x, or (1 - a) * x
+ * with `complement` (1 - a is computed from g, not from the rounded a).
+ *   dtype      CHOL_F32, CHOL_F16 or CHOL_BF16: the type of g, x and h.
+ *   g, x    in : element (b, t, c) at b * bs + t * ts + c of its own strides
+ *                (bs, ts in elements, ts >= d unless time <= 1), so that both may be
+ *                slices of one projection.
+ *   state0  in : (or NULL for zeros) float[sequences][d]: h before the first step.
+ *   offsets in : (or NULL) int64[nseq + 1] on the device, with batch = 1: the
+ *                time axis holds nseq sequences one behind another, sequence s
+ *                from offsets[s] to offsets[s + 1] (0 = offsets[0] <= ... <=
+ *                offsets[nseq] = time; a sequence may be empty, and its final
+ *                state is then its initial one).  Without offsets each row of
+ *                the batch is a sequence, and nseq is ignored.
+ *   h       out: dtype[batch][time][d].
+ *   state1  out: (or NULL) float[sequences][d], the last h of each sequence
+ *                before rounding.  May be state0 itself where time <= 1.
+ *   status  out: (or NULL) int32[1]: 0, or -1 where a bounded wait ran out
+ *                (h then holds NaN from there on).
+ *   work       as for chol_rms_norm_adj, of chol_linrec_workspace() bytes.
+ * Calls with time == 1 advance the states by one step (a token in serving).
+ */
+CHOL_API int chol_linrec(int64_t batch, int64_t time, int64_t d, int32_t dtype, int32_t gate_kind,
+                         int32_t complement, const void* g, int64_t g_bs, int64_t g_ts,
+                         const void* x, int64_t x_bs, int64_t x_ts, const float* state0,
+                         const int64_t* offsets, int64_t nseq, void* h, float* state1,
+                         int32_t* status, void* work, int64_t work_bytes, void* stream);
+
+/*
+ * chol_linrec_adj -- reverse mode, for gradients adj_h of h and adj_s1 of the
+ * final states:  lambda_t = adj_h_t + a_{t+1} lambda_{t+1}  (adj_s1 in place of
+ * the second term at a sequence's last step),
+ *     adj_a = lambda_t * (h_{t-1} - x_t with complement),   adj_g = adj_a * da/dg,
+ *     adj_x = lambda_t * (1 - a_t with complement),         adj_s0 = a_1 lambda_1.
+ *   g, x, state0, offsets as in the forward call (x may be NULL without
+ *   complement); h in: the forward's output; adj_h in: strides of its own;
+ *   adj_s1 in (or NULL for zeros): float[sequences][d].
+ *   adj_g, adj_x out: dtype[batch][time][d].   adj_s0 out (or NULL):
+ *   float[sequences][d].   status, work as in the forward call.
+ */
+CHOL_API int chol_linrec_adj(int64_t batch, int64_t time, int64_t d, int32_t dtype,
+                             int32_t gate_kind, int32_t complement, const void* g, int64_t g_bs,
+                             int64_t g_ts, const void* x, int64_t x_bs, int64_t x_ts,
+                             const float* state0, const int64_t* offsets, int64_t nseq,
+                             const void* h, const void* adj_h, int64_t adj_h_bs, int64_t adj_h_ts,
+                             const float* adj_s1, void* adj_g, void* adj_x, float* adj_s0,
+                             int32_t* status, void* work, int64_t work_bytes, void* stream);
+CHOL_API int64_t chol_linrec_workspace(int64_t batch, int64_t time, int64_t d, int32_t dtype);
+
+/* One tensor of an AdamW step. */
+typedef struct {
+    int64_t numel;
+    void* param;      /* param_dtype[numel], updated                                         */
+    const void* grad; /* grad_dtype[numel]                                                   */
+    void* m;          /* first moment:  float[numel], or E4M3 values [numel] with m_scale    */
+    void* v;          /* second moment: float[numel], or E4M3 values [numel] of its root     */
+    float* m_scale;   /* 8-bit moments: float[ceil(numel / 256)], else NULL                  */
+    float* v_scale;
+    void* copy;       /* (or NULL) grad_dtype[numel]: the updated parameter, rounded         */
+    double weight_decay;
+} chol_adamw_tensor;
+
+/*
+ * chol_adamw -- one step over `count` tensors:
+ *     g' = g * grad_scale,   m = beta1 m + (1 - beta1) g',   v = beta2 v + (1 - beta2) g'^2,
+ *     p = p (1 - lr weight_decay) - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps).
+ *   tensors       host array (read before the call returns).
+ *   param_dtype / grad_dtype: F32 with F32, F16 or BF16; F16 with F16; BF16 with
+ *                 BF16; F64 with F64 (the update is computed in float32 and
+ *                 subtracted in float64).  `copy` needs a 16-bit grad_dtype and
+ *                 F32 parameters.
+ *   state_bits    32 or 8.  With 8, every 256 consecutive elements of a tensor
+ *                 share a scale, their largest |m| (or sqrt(v)) over 448, at
+ *                 least 2^-100; a sqrt(v) above 0 is never rounded to 0.  The
+ *                 parameter's update uses the moments before they are rounded.
+ *                 A NaN or an infinity among a block's gradients makes its
+ *                 moments NaN: skip such steps with `status`.
+ *   step          from 1.
+ *   grad_scale    in : (or NULL for 1) float[1] on the device.
+ *   status        in : (or NULL) int32[1] on the device; where it is not 0 the
+ *                 step is skipped and nothing is written (a matrix that was not
+ *                 positive definite, a gradient that overflowed).
+ * Every multiplication, addition, square root and division is rounded by
+ * itself, so equal inputs give equal bits on every path.  No output may overlap
+ * another tensor's memory (CHOL_EALIAS).
+ */
+CHOL_API int chol_adamw(int64_t count, const chol_adamw_tensor* tensors, int32_t param_dtype,
+                        int32_t grad_dtype, int32_t state_bits, double lr, double beta1,
+                        double beta2, double eps, int64_t step, const float* grad_scale, const int32_t* status,
+                        void* stream);
+
+/* Version of this header: (major << 16) | minor. */
+CHOL_API int32_t chol_learn_version(void);
+
+#define CHOL_LEARN_VERSION ((1 << 16) | 0)
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* CHOL_LEARN_GB300_H */
