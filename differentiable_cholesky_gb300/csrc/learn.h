@@ -66,10 +66,7 @@ struct LinrecArgs {
     void* adj_g;
     void* adj_x;
     float* adj_s0;           // may be null
-    int32_t* status;         // may be null
-    void* work;              // linrec_workspace_bytes()
 };
-size_t linrec_workspace_bytes(int64_t batch, int64_t time, int64_t d, int32_t dtype);
 cudaError_t linrec(const LinrecArgs& a, int32_t dtype, int32_t gate, bool complement, bool adjoint,
                    cudaStream_t stream);
 

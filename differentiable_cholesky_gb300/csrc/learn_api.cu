@@ -113,7 +113,8 @@ int check_linrec(int64_t batch, int64_t time, int64_t d, int32_t dtype, int32_t 
     if (gate < CHOL_GATE_LINEAR || gate > CHOL_GATE_LOGIT) return CHOL_EINVAL;
     if (complement != 0 && complement != 1) return CHOL_EINVAL;
     if ((u128)batch * (u128)time * (u128)d * 4 > kMaxBytes) return CHOL_EINVAL;
-    if (offsets != nullptr && (batch != 1 || nseq < 0 || (nseq == 0 && time > 0)))
+    if (offsets != nullptr &&
+        (batch != 1 || nseq < 0 || nseq > INT32_MAX || (nseq == 0 && time > 0)))
         return CHOL_EINVAL;
     if ((u128)(offsets != nullptr ? nseq : batch) * (u128)d * 4 > kMaxBytes) return CHOL_EINVAL;
     for (int64_t s : bs)
@@ -133,8 +134,7 @@ u128 span3(int64_t batch, int64_t bs, int64_t time, int64_t ts, int64_t d, size_
 }
 
 // float[rows][d] copied, or zeros, where a recurrence has no steps.
-int copy_states(const float* from, float* to, int64_t rows, int64_t d, int32_t* status,
-                cudaStream_t s) {
+int copy_states(const float* from, float* to, int64_t rows, int64_t d, cudaStream_t s) {
     const size_t bytes = (size_t)rows * d * 4;
     if (to != nullptr && to != from && bytes > 0) {
         const cudaError_t e = from != nullptr
@@ -142,7 +142,6 @@ int copy_states(const float* from, float* to, int64_t rows, int64_t d, int32_t* 
                                   : cudaMemsetAsync(to, 0, bytes, s);
         if (e != cudaSuccess) return CHOL_ECUDA;
     }
-    if (status != nullptr && cudaMemsetAsync(status, 0, 4, s) != cudaSuccess) return CHOL_ECUDA;
     return CHOL_OK;
 }
 
@@ -230,52 +229,36 @@ int chol_rms_norm_adj(int64_t rows, int64_t d, int32_t dtype, int32_t r_dtype, c
         dtype, r_dtype, s)));
 }
 
-int64_t chol_linrec_workspace(int64_t batch, int64_t time, int64_t d, int32_t dtype) {
-    if (model_size(dtype) == 0) return CHOL_EDTYPE;
-    if (batch < 0 || time < 0 || d <= 0 || d > kMaxD ||
-        (u128)batch * (u128)time * (u128)d * 4 > kMaxBytes)
-        return CHOL_EINVAL;
-    return (int64_t)chol::linrec_workspace_bytes(batch, time, d, dtype);
-}
-
 int chol_linrec(int64_t batch, int64_t time, int64_t d, int32_t dtype, int32_t gate_kind,
                 int32_t complement, const void* g, int64_t g_bs, int64_t g_ts, const void* x,
                 int64_t x_bs, int64_t x_ts, const float* state0, const int64_t* offsets,
-                int64_t nseq, void* h, float* state1, int32_t* status, void* work,
-                int64_t work_bytes, void* stream) {
+                int64_t nseq, void* h, float* state1, void* stream) {
     int rc = check_linrec(batch, time, d, dtype, gate_kind, complement, {g_bs, x_bs}, {g_ts, x_ts},
                           offsets, nseq);
     if (rc != CHOL_OK) return rc;
     if (offsets == nullptr) nseq = batch;
     if (nseq == 0) return CHOL_OK;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (!usable_or_null(state0, 4) || !usable_or_null(offsets, 8) || !usable_or_null(state1, 4) ||
-        !usable_or_null(status, 4) || !work_ok(work, work_bytes))
+    if (!usable_or_null(state0, 4) || !usable_or_null(offsets, 8) || !usable_or_null(state1, 4))
         return CHOL_EINVAL;
     const size_t es = model_size(dtype);
     if (time > 0 && (!usable(g, es) || !usable(x, es) || !usable(h, es))) return CHOL_EINVAL;
-    const size_t need = chol::linrec_workspace_bytes(batch, time, d, dtype);
     const u128 states = (u128)nseq * d * 4;
     if (aliased({{g, span3(batch, g_bs, time, g_ts, d, es), false, nullptr},
                  {x, span3(batch, x_bs, time, x_ts, d, es), false, nullptr},
                  {state0, states, false, nullptr},
                  {offsets, (u128)(nseq + 1) * 8, false, nullptr},
                  {h, (u128)batch * time * d * es, true, nullptr},
-                 {state1, states, true, time <= 1 ? state0 : nullptr},
-                 {status, 4, true, nullptr},
-                 {work, need, true, nullptr}}))
+                 {state1, states, true, time <= 1 ? state0 : nullptr}}))
         return CHOL_EALIAS;
-    if (time == 0) return copy_states(state0, state1, nseq, d, status, s);
-    Work scratch(s);
-    void* mem = nullptr;
-    if ((rc = scratch.get(work, work_bytes, need, &mem)) != CHOL_OK) return rc;
+    if (time == 0) return copy_states(state0, state1, nseq, d, s);
     chol::LinrecArgs a = {};
     a.batch = batch, a.time = time, a.d = d;
     a.g = g, a.g_bs = g_bs, a.g_ts = g_ts;
     a.x = x, a.x_bs = x_bs, a.x_ts = x_ts;
     a.state0 = state0, a.offsets = offsets, a.nseq = nseq;
-    a.h = h, a.state1 = state1, a.status = status, a.work = mem;
-    return scratch.done(to_code(chol::linrec(a, dtype, gate_kind, complement != 0, false, s)));
+    a.h = h, a.state1 = state1;
+    return to_code(chol::linrec(a, dtype, gate_kind, complement != 0, false, s));
 }
 
 int chol_linrec_adj(int64_t batch, int64_t time, int64_t d, int32_t dtype, int32_t gate_kind,
@@ -283,7 +266,7 @@ int chol_linrec_adj(int64_t batch, int64_t time, int64_t d, int32_t dtype, int32
                     int64_t x_bs, int64_t x_ts, const float* state0, const int64_t* offsets,
                     int64_t nseq, const void* h, const void* adj_h, int64_t adj_h_bs,
                     int64_t adj_h_ts, const float* adj_s1, void* adj_g, void* adj_x, float* adj_s0,
-                    int32_t* status, void* work, int64_t work_bytes, void* stream) {
+                    void* stream) {
     const bool has_x = complement != 0;
     int rc = check_linrec(batch, time, d, dtype, gate_kind, complement,
                           {g_bs, has_x ? x_bs : 0, adj_h_bs}, {g_ts, has_x ? x_ts : d, adj_h_ts},
@@ -293,13 +276,12 @@ int chol_linrec_adj(int64_t batch, int64_t time, int64_t d, int32_t dtype, int32
     if (nseq == 0) return CHOL_OK;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (!usable_or_null(state0, 4) || !usable_or_null(offsets, 8) || !usable_or_null(adj_s1, 4) ||
-        !usable_or_null(adj_s0, 4) || !usable_or_null(status, 4) || !work_ok(work, work_bytes))
+        !usable_or_null(adj_s0, 4))
         return CHOL_EINVAL;
     const size_t es = model_size(dtype);
     if (time > 0 && (!usable(g, es) || (has_x && !usable(x, es)) || !usable(h, es) ||
                      !usable(adj_h, es) || !usable(adj_g, es) || !usable(adj_x, es)))
         return CHOL_EINVAL;
-    const size_t need = chol::linrec_workspace_bytes(batch, time, d, dtype);
     const u128 states = (u128)nseq * d * 4, n = (u128)batch * time * d * es;
     if (aliased({{g, span3(batch, g_bs, time, g_ts, d, es), false, nullptr},
                  {has_x ? x : nullptr, span3(batch, x_bs, time, x_ts, d, es), false, nullptr},
@@ -310,14 +292,9 @@ int chol_linrec_adj(int64_t batch, int64_t time, int64_t d, int32_t dtype, int32
                  {adj_s1, states, false, nullptr},
                  {adj_g, n, true, nullptr},
                  {adj_x, n, true, nullptr},
-                 {adj_s0, states, true, nullptr},
-                 {status, 4, true, nullptr},
-                 {work, need, true, nullptr}}))
+                 {adj_s0, states, true, nullptr}}))
         return CHOL_EALIAS;
-    if (time == 0) return copy_states(adj_s1, adj_s0, nseq, d, status, s);
-    Work scratch(s);
-    void* mem = nullptr;
-    if ((rc = scratch.get(work, work_bytes, need, &mem)) != CHOL_OK) return rc;
+    if (time == 0) return copy_states(adj_s1, adj_s0, nseq, d, s);
     chol::LinrecArgs a = {};
     a.batch = batch, a.time = time, a.d = d;
     a.g = g, a.g_bs = g_bs, a.g_ts = g_ts;
@@ -326,8 +303,7 @@ int chol_linrec_adj(int64_t batch, int64_t time, int64_t d, int32_t dtype, int32
     a.h = const_cast<void*>(h);
     a.adj_h = adj_h, a.dh_bs = adj_h_bs, a.dh_ts = adj_h_ts;
     a.adj_s1 = adj_s1, a.adj_g = adj_g, a.adj_x = adj_x, a.adj_s0 = adj_s0;
-    a.status = status, a.work = mem;
-    return scratch.done(to_code(chol::linrec(a, dtype, gate_kind, complement != 0, true, s)));
+    return to_code(chol::linrec(a, dtype, gate_kind, complement != 0, true, s));
 }
 
 int chol_adamw(int64_t count, const chol_adamw_tensor* tensors, int32_t param_dtype,

@@ -48,17 +48,14 @@ def _library():
                                           vp, vp, i64, vp]
         lib.chol_rms_norm_adj_workspace.argtypes = [i64, i64]
         lib.chol_linrec.argtypes = [i64, i64, i64, i32, i32, i32, vp, i64, i64, vp, i64, i64, vp,
-                                    vp, i64, vp, vp, vp, vp, i64, vp]
+                                    vp, i64, vp, vp, vp]
         lib.chol_linrec_adj.argtypes = [i64, i64, i64, i32, i32, i32, vp, i64, i64, vp, i64, i64,
-                                        vp, vp, i64, vp, vp, i64, i64, vp, vp, vp, vp, vp, vp,
-                                        i64, vp]
-        lib.chol_linrec_workspace.argtypes = [i64, i64, i64, i32]
+                                        vp, vp, i64, vp, vp, i64, i64, vp, vp, vp, vp, vp]
         lib.chol_adamw.argtypes = [i64, vp, i32, i32, i32, f64, f64, f64, f64, i64, vp, vp, vp]
         for f in (lib.chol_rms_norm, lib.chol_rms_norm_adj, lib.chol_linrec, lib.chol_linrec_adj,
                   lib.chol_adamw):
             f.restype = ctypes.c_int
-        for f in (lib.chol_rms_norm_adj_workspace, lib.chol_linrec_workspace):
-            f.restype = i64
+        lib.chol_rms_norm_adj_workspace.restype = i64
         lib.chol_learn_version.argtypes = []
         lib.chol_learn_version.restype = i32
         _lib = lib
@@ -324,13 +321,6 @@ def _recurrence(gate, x, state, offsets, kind):
     return shape, strides, n
 
 
-def _work(lib, shape, x):
-    need = lib.chol_linrec_workspace(shape[0], shape[1], shape[2], _MODEL[x.dtype])
-    if need <= 0:
-        return None, 0
-    return torch.empty(need, dtype=torch.uint8, device=x.device), need
-
-
 def linrec_fwd(gate: torch.Tensor, x: torch.Tensor, state: torch.Tensor | None = None,
                offsets: torch.Tensor | None = None, kind: str = "logit", complement: bool = True,
                stream=None):
@@ -350,11 +340,10 @@ def linrec_fwd(gate: torch.Tensor, x: torch.Tensor, state: torch.Tensor | None =
         lib = _library()
         h = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         last = torch.empty((n, d), dtype=torch.float32, device=x.device)
-        work, need = _work(lib, shape, x)
         _check(lib.chol_linrec(
             batch, time, d, _MODEL[x.dtype], _GATES[kind], int(complement), gate.data_ptr(), gbs,
             gts, x.data_ptr(), bs, ts, _ptr(state), _ptr(offsets), n, h.data_ptr(),
-            last.data_ptr(), None, _ptr(work), need, _b._stream_ptr(stream)))
+            last.data_ptr(), _b._stream_ptr(stream)))
         return h, last
 
     return _on(stream, (gate, x, state, offsets), call)
@@ -384,7 +373,7 @@ def linrec_step(gate: torch.Tensor, x: torch.Tensor, state: torch.Tensor, kind: 
         _check(_library().chol_linrec(
             batch, 1, d, _MODEL[x.dtype], _GATES[kind], int(complement), gate.data_ptr(),
             gate.stride(0), d, x.data_ptr(), x.stride(0), d, state.data_ptr(), None, batch,
-            h.data_ptr(), state.data_ptr(), None, None, 0, _b._stream_ptr(stream)))
+            h.data_ptr(), state.data_ptr(), _b._stream_ptr(stream)))
         return h
 
     return _on(stream, (gate, x, state), call)
@@ -412,12 +401,11 @@ def linrec_adj(gate: torch.Tensor, x: torch.Tensor, h: torch.Tensor, adj_h: torc
         adj_g = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         adj_x = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         adj_0 = torch.empty((n, d), dtype=torch.float32, device=x.device)
-        work, need = _work(lib, shape, x)
         _check(lib.chol_linrec_adj(
             batch, time, d, _MODEL[x.dtype], _GATES[kind], int(complement), gate.data_ptr(), gbs,
             gts, x.data_ptr(), bs, ts, _ptr(state), _ptr(offsets), n, h.data_ptr(),
             adj_h.data_ptr(), dbs, dts, _ptr(adj_state), adj_g.data_ptr(), adj_x.data_ptr(),
-            adj_0.data_ptr(), None, _ptr(work), need, _b._stream_ptr(stream)))
+            adj_0.data_ptr(), _b._stream_ptr(stream)))
         return adj_g, adj_x, adj_0
 
     return _on(stream, (gate, x, h, adj_h, state, adj_state, offsets), call)

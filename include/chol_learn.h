@@ -119,16 +119,14 @@ CHOL_API int64_t chol_rms_norm_adj_workspace(int64_t rows, int64_t d);
  *   h       out: dtype[batch][time][d].
  *   state1  out: (or NULL) float[sequences][d], the last h of each sequence
  *                before rounding.  May be state0 itself where time <= 1.
- *   status  out: (or NULL) int32[1]: 0, or -1 where a bounded wait ran out
- *                (h then holds NaN from there on).
- *   work       as for chol_rms_norm_adj, of chol_linrec_workspace() bytes.
  * Calls with time == 1 advance the states by one step (a token in serving).
+ * No call takes a workspace.  At most 2^31 - 1 sequences.
  */
 CHOL_API int chol_linrec(int64_t batch, int64_t time, int64_t d, int32_t dtype, int32_t gate_kind,
                          int32_t complement, const void* g, int64_t g_bs, int64_t g_ts,
                          const void* x, int64_t x_bs, int64_t x_ts, const float* state0,
                          const int64_t* offsets, int64_t nseq, void* h, float* state1,
-                         int32_t* status, void* work, int64_t work_bytes, void* stream);
+                         void* stream);
 
 /*
  * chol_linrec_adj -- reverse mode, for gradients adj_h of h and adj_s1 of the
@@ -140,7 +138,7 @@ CHOL_API int chol_linrec(int64_t batch, int64_t time, int64_t d, int32_t dtype, 
  *   complement); h in: the forward's output; adj_h in: strides of its own;
  *   adj_s1 in (or NULL for zeros): float[sequences][d].
  *   adj_g, adj_x out: dtype[batch][time][d].   adj_s0 out (or NULL):
- *   float[sequences][d].   status, work as in the forward call.
+ *   float[sequences][d].
  */
 CHOL_API int chol_linrec_adj(int64_t batch, int64_t time, int64_t d, int32_t dtype,
                              int32_t gate_kind, int32_t complement, const void* g, int64_t g_bs,
@@ -148,8 +146,7 @@ CHOL_API int chol_linrec_adj(int64_t batch, int64_t time, int64_t d, int32_t dty
                              const float* state0, const int64_t* offsets, int64_t nseq,
                              const void* h, const void* adj_h, int64_t adj_h_bs, int64_t adj_h_ts,
                              const float* adj_s1, void* adj_g, void* adj_x, float* adj_s0,
-                             int32_t* status, void* work, int64_t work_bytes, void* stream);
-CHOL_API int64_t chol_linrec_workspace(int64_t batch, int64_t time, int64_t d, int32_t dtype);
+                             void* stream);
 
 /* One tensor of an AdamW step. */
 typedef struct {

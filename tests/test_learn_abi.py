@@ -77,9 +77,9 @@ def test_linrec_arguments(lib):
     keep, p = host()
 
     def call(batch=1, time=2, d=4, dtype=F32, gate=2, comp=1, g=p, gbs=8, gts=4, x=p, xbs=8, xts=4,
-             s0=None, off=None, n=0, h=p, s1=None, status=None, work=None, size=0):
+             s0=None, off=None, n=0, h=p, s1=None):
         return lib.chol_linrec(batch, time, d, dtype, gate, comp, g, gbs, gts, x, xbs, xts, s0, off,
-                               n, h, s1, status, work, size, None)
+                               n, h, s1, None)
 
     assert call(dtype=F64) == EDTYPE and call(dtype=E4M3) == EDTYPE
     assert call(batch=-1) == EINVAL and call(time=-1) == EINVAL and call(d=0) == EINVAL
@@ -91,9 +91,7 @@ def test_linrec_arguments(lib):
     assert call() == EINVAL                               # host memory
     assert call(g=None) == EINVAL
     assert call(batch=0, g=None, x=None, h=None) == OK
-    assert lib.chol_linrec_workspace(1, 1, 1, F64) == EDTYPE
-    assert lib.chol_linrec_workspace(-1, 1, 1, F32) == EINVAL
-    assert lib.chol_linrec_workspace(4, 1, 64, BF16) == 0  # a single step needs none
+    assert call(off=p, n=1 << 31) == EINVAL
 
 
 def test_linrec_adj_arguments(lib):
@@ -101,7 +99,7 @@ def test_linrec_adj_arguments(lib):
 
     def call(batch=1, time=2, d=4, dtype=F32, gate=2, comp=1, x=p, xts=4, dts=4, h=p, dh=p, dg=p, dx=p):
         return lib.chol_linrec_adj(batch, time, d, dtype, gate, comp, p, 8, 4, x, 8, xts, None, None,
-                                   0, h, dh, 8, dts, None, dg, dx, None, None, None, 0, None)
+                                   0, h, dh, 8, dts, None, dg, dx, None, None)
 
     assert call(dtype=I8) == EDTYPE and call(gate=5) == EINVAL and call(comp=-1) == EINVAL
     assert call(xts=2) == EINVAL and call(dts=2) == EINVAL
@@ -220,10 +218,10 @@ def test_overlapping_outputs_are_refused():
     assert lib.chol_rms_norm(4, 64, 0, 0, 0, 0, 1e-6, p, 64, None, 0, None, p + 8192, None,
                              p + 8192 + 512, None, None) == -3
     assert lib.chol_linrec(1, 4, 64, 0, 2, 1, p, 256, 64, p + 1024, 256, 64, None, None, 0, p + 512,
-                           None, None, None, 0, None) == -3
+                           None, None) == -3
     # final states over initial ones: a single step only
     assert lib.chol_linrec(1, 2, 64, 0, 2, 1, p, 128, 64, p + 1024, 128, 64, p + 4096, None, 0,
-                           p + 8192, p + 4096, None, None, 0, None) == -3
+                           p + 8192, p + 4096, None) == -3
     w = buf[:100]
     with pytest.raises(CholError):
         learn.AdamW([w, buf[50:150]]).step([buf[1000:1100], buf[2000:2100]])
