@@ -10,10 +10,11 @@
 //     same channels scan their maps with shuffles, and the warps' maps meet in
 //     shared memory;
 //   - a cluster of up to 8 thread blocks takes as many tiles at once: every
-//     block sends its tile's map to the others' shared memory, and after one
-//     cluster barrier each applies the maps before its own to the state that
-//     it carries from tile to tile.  No block waits on global memory, and no
-//     other cluster's work is waited for;
+//     block sends its tile's map to the others' shared memory, where an
+//     mbarrier counts the bytes, and each applies the maps before its own to
+//     the state that it carries from round to round.  No block waits on global
+//     memory, nor on another cluster (the wait has a limit all the same; past
+//     it the states become NaN);
 //   - the threads run their steps again from the state before them, which is
 //     known now, and write.
 // So every input is read once, and the next tile's inputs are on their way
@@ -26,6 +27,13 @@
 // The adjoint is the same recurrence walked from the end, on the carry
 // a_t lambda_t:  lambda_t = adj_h_t + carry_{t+1}.
 #pragma once
+#ifndef CHOL_LR_V
+#define CHOL_LR_V V
+#define CHOL_LR_CX 8
+#define CHOL_LR_LSF 4
+#define CHOL_LR_LSA 2
+#define CHOL_LR_OCC 2
+#endif
 
 #include "learn.cuh"
 #include "learn.h"
@@ -46,7 +54,7 @@ template <int GATE> __device__ __forceinline__ void gate(float g, float& a, floa
         a = g;
         c = 1.0f - g;
     } else if constexpr (GATE == CHOL_GATE_LOG) {
-        a = __expf(g);
+        a = exp2_fast(g * 1.44269504f);
         float p = 1.0f / 5040.0f;
         p = fmaf(p, g, 1.0f / 720.0f);
         p = fmaf(p, g, 1.0f / 120.0f);
@@ -56,33 +64,42 @@ template <int GATE> __device__ __forceinline__ void gate(float g, float& a, floa
         p = fmaf(p, g, 1.0f);
         c = fabsf(g) < 0.35f ? -p * g : 1.0f - a;
     } else {
-        const float e = __expf(-g);  // infinity gives a = 0, c = 1
-        a = __frcp_rn(1.0f + e);
+        const float e = exp2_fast(g * -1.44269504f);  // infinity gives a = 0, c = 1
+        a = rcp_fast(1.0f + e);
         c = e > 1.0f ? 1.0f - a : e * a;
     }
 }
 
-// V elements of a row as they lie in memory.
+// V elements of a row as they lie in memory: 8 or 16 bytes.
 template <typename T, int V> struct Raw {
     static constexpr int kWords = V * (int)sizeof(T) / 4;
     uint32_t w[kWords];
     __device__ __forceinline__ void load(const T* p, bool ok) {
-        uint4 q = make_uint4(0, 0, 0, 0);
-        if (ok) q = __ldg(reinterpret_cast<const uint4*>(p));
-        w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+        if constexpr (kWords == 4) {
+            uint4 q = make_uint4(0, 0, 0, 0);
+            if (ok) q = __ldg(reinterpret_cast<const uint4*>(p));
+            w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+        } else {
+            uint2 q = make_uint2(0, 0);
+            if (ok) q = __ldg(reinterpret_cast<const uint2*>(p));
+            w[0] = q.x, w[1] = q.y;
+        }
     }
-    __device__ __forceinline__ float get(int v) const {
-        if constexpr (sizeof(T) == 4) return __uint_as_float(w[v]);
-        else return to_f32(reinterpret_cast<const T*>(w)[v]);
+    __device__ __forceinline__ void get(float (&f)[V]) const {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            if constexpr (sizeof(T) == 4) f[i] = __uint_as_float(w[i]);
+            else unpack2<T>(w[i], f[2 * i], f[2 * i + 1]);
+        }
     }
 };
 template <typename T> struct Raw<T, 1> {
     T x;
     __device__ __forceinline__ void load(const T* p, bool ok) {
         x = from_f32<T>(0.0f);
-        if (ok) x = *p;
+        if (ok) x = __ldg(p);
     }
-    __device__ __forceinline__ float get(int) const { return to_f32(x); }
+    __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = to_f32(x); }
 };
 
 template <typename T, int V>
@@ -90,10 +107,14 @@ __device__ __forceinline__ void store(T* p, const float (&v)[V]) {
     if constexpr (V == 1) {
         *p = from_f32<T>(v[0]);
     } else {
-        alignas(16) T t[V];
+        uint32_t w[V * sizeof(T) / 4];
 #pragma unroll
-        for (int i = 0; i < V; ++i) t[i] = from_f32<T>(v[i]);
-        *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(t);
+        for (int i = 0; i < (int)(V * sizeof(T) / 4); ++i) {
+            if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(v[i]);
+            else w[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
+        }
+        if constexpr (V * sizeof(T) == 16) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        else *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
     }
 }
 
@@ -112,23 +133,46 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void cluster_arrive() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+// All blocks of the cluster have come here (memory is not ordered by it).
+__device__ __forceinline__ void cluster_meet() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 // Stores into the shared memory of block `rank` of the cluster, at the
-// address that `p` has here.
-__device__ __forceinline__ void put(float2* p, uint32_t rank, float2 v) {
-    uint32_t at;
+// addresses that `p` and `bar` have here: the bytes are counted on `bar` when
+// they are there.  No fence is needed, so the tile before may still be on
+// its way to memory.
+__device__ __forceinline__ void send(float2* p, uint64_t* bar, uint32_t rank, float2 v) {
+    uint32_t at, on;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
-    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(v.x), "f"(v.y) : "memory");
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(on) : "r"(smem_u32(bar)), "r"(rank));
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::
+                     "r"(at), "f"(v.x), "f"(v.y), "r"(on)
+                 : "memory");
 }
-__device__ __forceinline__ void put(int* p, uint32_t rank, int v) {
-    uint32_t at;
+__device__ __forceinline__ void send(int* p, uint64_t* bar, uint32_t rank, int v) {
+    uint32_t at, on;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(on) : "r"(smem_u32(bar)), "r"(rank));
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::
+                     "r"(at), "r"(v), "r"(on)
+                 : "memory");
+}
+
+// Waits for a phase of `bar` and for what was sent with it; gives up (false)
+// after a number of polls.
+__device__ __forceinline__ bool wait_maps(uint64_t* bar, uint32_t parity) {
+    for (uint32_t i = 0; i < (1u << 18); ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+        if (ok) return true;
+    }
+    return false;
 }
 
 // Steps of a tile that begin or end a sequence, as the tile is walked: the
@@ -164,7 +208,7 @@ __device__ __forceinline__ void mark(const LinrecArgs& a, int64_t lo, int64_t hi
 // number of channel blocks of a row.  All blocks of a cluster go through the
 // same number of barriers.
 template <typename T, int V, int CX, int LS, int GATE, bool ADJ, bool PACKED>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, CHOL_LR_OCC)
 linrec_tile_kernel(const LinrecArgs a, const bool comp, const int64_t blocks, const int cs) {
     constexpr int C = CX * V;         // channels
     constexpr int TW = 32 / CX;       // threads of a warp along time
@@ -174,6 +218,7 @@ linrec_tile_kernel(const LinrecArgs a, const bool comp, const int64_t blocks, co
     __shared__ __align__(16) float warp_state[kWarps][C];
     __shared__ int warp_cut[kWarps], tile_cut[2][kMaxCluster];
     __shared__ int marks[PACKED ? 2 : 1][2][PACKED ? L : 1];
+    __shared__ uint64_t arrived[2];  // the maps of a round, by its parity
 
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int cx = lane % CX, tw = lane / CX;
@@ -182,25 +227,39 @@ linrec_tile_kernel(const LinrecArgs a, const bool comp, const int64_t blocks, co
     const int64_t U = a.time;
     const int64_t tiles = (U + L - 1) / L, rounds = (tiles + cs - 1) / cs;
     const int64_t total = a.batch * blocks;
-    auto t_of = [&](int64_t u) { return ADJ ? U - 1 - u : u; };
+    const int64_t round_steps = (int64_t)cs * L;
     const float* state_in = ADJ ? a.adj_s1 : a.state0;
     float* state_out = ADJ ? a.adj_s0 : a.state1;
+    // a step later, as the axis is walked, in elements of each array
+    const int64_t sg = ADJ ? -a.g_ts : a.g_ts, sx = ADJ ? -a.x_ts : a.x_ts, sd = -a.dh_ts;
+    const int64_t so = ADJ ? -a.d : a.d;
 
-    if (cs > 1) cluster_arrive();  // every block of the cluster has started ...
     if constexpr (PACKED) {
         for (int i = threadIdx.x; i < 2 * L; i += kThreads) (&marks[0][0][0])[i] = -1;
-        __syncthreads();
     }
-    if (cs > 1) cluster_wait();    // ... before one writes to another
+    if (threadIdx.x == 0) {
+        mbar_init(&arrived[0], 1);
+        mbar_init(&arrived[1], 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    if (cs > 1) cluster_meet();  // before one block writes to another
+    const uint32_t round_bytes = (uint32_t)cs * (C * (uint32_t)sizeof(float2) + (PACKED ? 4u : 0u));
     int buf = 0;
+    uint32_t parity = 0;   // of the round's wait: changes every second round
+    bool lost = false;     // a wait ran out: the states are NaN from there on
     for (int64_t job = blockIdx.x / cs; job < total; job += gridDim.x / cs) {
         const int64_t b = job / blocks;
         const int64_t c = (job % blocks) * C + cx * V;
         const bool here = c < a.d;
-        const T* g = static_cast<const T*>(a.g) + b * a.g_bs + c;
-        const T* x = static_cast<const T*>(a.x) + b * a.x_bs + c;
-        const T* h_in = static_cast<const T*>(a.h) + b * U * a.d + c;
-        const T* dh = static_cast<const T*>(a.adj_h) + b * a.dh_bs + c;
+        // this thread's first step of the tile that is fetched next
+        int64_t u0 = (int64_t)rank * L + row0;
+        const int64_t t0 = ADJ ? U - 1 - u0 : u0;
+        const T* g = static_cast<const T*>(a.g) + b * a.g_bs + c + t0 * a.g_ts;
+        const T* x = static_cast<const T*>(a.x) + b * a.x_bs + c + t0 * a.x_ts;
+        const T* dh = ADJ ? static_cast<const T*>(a.adj_h) + b * a.dh_bs + c + t0 * a.dh_ts : nullptr;
+        int64_t o = (b * U + t0) * a.d + c;  // of the contiguous arrays
+        const T* h_before = ADJ ? static_cast<const T*>(a.h) + o - a.d : nullptr;
         const bool want_x = !ADJ || comp;
 
         // the state before the tiles of a round, of one channel per thread
@@ -209,32 +268,38 @@ linrec_tile_kernel(const LinrecArgs a, const bool comp, const int64_t blocks, co
         if (!PACKED && threadIdx.x < C && own < a.d && state_in != nullptr)
             running = state_in[b * a.d + own];
 
+        // Steps of this thread that there are, of a tile whose first is u.
+        // The others, all behind the last, are fetched as zeros and give
+        // states that nothing reads.
+        auto steps_at = [&](int64_t u) {
+            return here ? (int)max((int64_t)0, min((int64_t)LS, U - u)) : 0;
+        };
         Raw<T, V> rg[LS], rx[LS], rd[ADJ ? LS : 1], rh[ADJ ? LS : 1];
-        auto fetch = [&](int64_t tile) {
-            const int64_t u0 = tile * L + row0;
+        auto fetch = [&](int64_t u) {
+            const int n = steps_at(u);
 #pragma unroll
             for (int i = 0; i < LS; ++i) {
-                const int64_t u = u0 + i, t = t_of(u);
-                const bool ok = here && u < U;
-                rg[i].load(g + t * a.g_ts, ok);
+                rg[i].load(g + i * sg, i < n);
                 if constexpr (ADJ) {
-                    rd[i].load(dh + t * a.dh_ts, ok);
-                    rh[i].load(h_in + (t - 1) * a.d, ok && t > 0);
+                    rd[i].load(dh + i * sd, i < n);
+                    rh[i].load(h_before + i * so, i < n && u + i < U - 1);
                 }
-                rx[i].load(x + t * a.x_ts, ok && want_x);
+                rx[i].load(x + i * sx, i < n && want_x);
             }
+            g += round_steps * sg;
+            x += round_steps * sx;
+            if constexpr (ADJ) dh += round_steps * sd, h_before += round_steps * so;
         };
-        fetch(rank);
-        for (int64_t round = 0; round < rounds; ++round) {
-            const int64_t tile = round * cs + rank;
-            const int64_t u0 = tile * L + row0;
+        fetch(u0);
+        for (int64_t round = 0; round < rounds; ++round, u0 += round_steps, o += round_steps * so) {
             int *enter = nullptr, *leave = nullptr;
             if constexpr (PACKED) {
                 enter = marks[buf][0], leave = marks[buf][1];
-                const int64_t first = tile * L, last = min(first + L, U);
+                const int64_t first = u0 - row0, last = min(first + L, U);
                 if (first < U) {
-                    const int64_t lo = ADJ ? t_of(last - 1) : first, hi = ADJ ? t_of(first) + 1 : last;
-                    mark<ADJ>(a, lo, hi, {enter, leave}, [&](int64_t t) { return (int)(t_of(t) - first); });
+                    const int64_t lo = ADJ ? U - last : first, hi = ADJ ? U - first : last;
+                    mark<ADJ>(a, lo, hi, {enter, leave},
+                              [&](int64_t t) { return (int)((ADJ ? U - 1 - t : t) - first); });
                 }
                 __syncthreads();
                 // the other buffer is for the next tile; its readers are all past it
@@ -247,7 +312,6 @@ linrec_tile_kernel(const LinrecArgs a, const bool comp, const int64_t blocks, co
             for (int v = 0; v < V; ++v) A[v] = 1.0f, H[v] = 0.0f;
 #pragma unroll
             for (int i = 0; i < LS; ++i) {
-                const bool in = u0 + i < U;
                 if constexpr (PACKED) {
                     const int s = enter[row0 + i];
                     if (s >= 0) {
@@ -255,17 +319,14 @@ linrec_tile_kernel(const LinrecArgs a, const bool comp, const int64_t blocks, co
                         load_state<V>(state_in != nullptr && here ? state_in + s * a.d + c : nullptr, H);
                     }
                 }
+                float gv[V];
+                rg[i].get(gv);
+                if constexpr (ADJ) rd[i].get(bv[i]); else rx[i].get(bv[i]);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     float cv;
-                    gate<GATE>(rg[i].get(v), av[i][v], cv);
-                    if constexpr (!ADJ) {
-                        const float xv = rx[i].get(v);
-                        bv[i][v] = comp ? cv * xv : xv;
-                    } else {
-                        bv[i][v] = rd[i].get(v);
-                    }
-                    if (!in) av[i][v] = 1.0f, bv[i][v] = 0.0f;
+                    gate<GATE>(gv[v], av[i][v], cv);
+                    if (!ADJ && comp) bv[i][v] *= cv;
                     H[v] = ADJ ? av[i][v] * (bv[i][v] + H[v]) : fmaf(av[i][v], H[v], bv[i][v]);
                     A[v] *= av[i][v];
                 }
@@ -276,23 +337,23 @@ linrec_tile_kernel(const LinrecArgs a, const bool comp, const int64_t blocks, co
 #pragma unroll
                 for (int i = 0; i < LS; ++i) kg[i] = rg[i], kx[i] = rx[i], kh[i] = rh[i];
             }
-            if (round + 1 < rounds) fetch(tile + cs);
+            if (round + 1 < rounds) fetch(u0 + round_steps);
 
             // maps of all steps of the warp up to and with this thread's
             int cuts = cut;
 #pragma unroll
-            for (int o = 1; o < TW; o *= 2) {
-                const int pc = PACKED ? __shfl_up_sync(0xffffffffu, cuts, o * CX) : 0;
+            for (int k = 1; k < TW; k *= 2) {
+                const int pc = PACKED ? __shfl_up_sync(0xffffffffu, cuts, k * CX) : 0;
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    const float pa = __shfl_up_sync(0xffffffffu, A[v], o * CX);
-                    const float ph = __shfl_up_sync(0xffffffffu, H[v], o * CX);
-                    if (tw >= o && !(PACKED && cuts)) {
+                    const float pa = __shfl_up_sync(0xffffffffu, A[v], k * CX);
+                    const float ph = __shfl_up_sync(0xffffffffu, H[v], k * CX);
+                    if (tw >= k && !(PACKED && cuts)) {
                         H[v] = fmaf(A[v], ph, H[v]);
                         A[v] *= pa;
                     }
                 }
-                if (PACKED && tw >= o) cuts |= pc;
+                if (PACKED && tw >= k) cuts |= pc;
             }
             if (tw == TW - 1) {
 #pragma unroll
@@ -331,19 +392,21 @@ linrec_tile_kernel(const LinrecArgs a, const bool comp, const int64_t blocks, co
                             ma *= m.x;
                         }
                     }
+                    if (threadIdx.x == 0) mbar_arrive_expect_tx(&arrived[buf], round_bytes);
                     for (int r = 0; r < cs; ++r) {
-                        put(&tile_map[buf][rank][threadIdx.x], r, make_float2(ma, mh));
-                        if (PACKED && threadIdx.x == 0) put(&tile_cut[buf][rank], r, mc);
+                        send(&tile_map[buf][rank][threadIdx.x], &arrived[buf], r, make_float2(ma, mh));
+                        if (PACKED && threadIdx.x == 0) send(&tile_cut[buf][rank], &arrived[buf], r, mc);
                     }
-                }
-                cluster_arrive();
-                cluster_wait();
-                if (threadIdx.x < C) {
+                    // A block sends the maps of the round after next only when it
+                    // has this block's of the next, so a buffer is never
+                    // overwritten while it is read.
+                    lost = lost || !wait_maps(&arrived[buf], parity);
                     for (int r = 0; r < cs; ++r) {
                         if (r == (int)rank) s = running;
                         const float2 m = tile_map[buf][r][threadIdx.x];
                         running = PACKED && tile_cut[buf][r] ? m.y : fmaf(m.x, running, m.y);
                     }
+                    if (lost) s = running = __int_as_float(0x7fffffff);
                 }
             }
             if (threadIdx.x < C) {
@@ -363,48 +426,48 @@ linrec_tile_kernel(const LinrecArgs a, const bool comp, const int64_t blocks, co
                 st[v] = warp_state[warp][cx * V + v];
                 st[v] = PACKED && cuts ? H[v] : fmaf(A[v], st[v], H[v]);
             }
+            const int n = steps_at(u0);
 #pragma unroll
             for (int i = 0; i < LS; ++i) {
-                const int64_t u = u0 + i, t = t_of(u);
-                if (!here || u >= U) break;
+                if (i >= n) break;
                 int64_t leaving = -1;
                 if constexpr (PACKED) {
                     const int e = enter[row0 + i];
                     if (e >= 0) load_state<V>(state_in != nullptr ? state_in + e * a.d + c : nullptr, st);
                     leaving = leave[row0 + i];
                 } else {
-                    if (u == U - 1) leaving = b;
+                    if (u0 + i == U - 1) leaving = b;
                 }
-                const int64_t o = (b * U + t) * a.d + c;
+                const int64_t at = o + i * so;
                 if constexpr (!ADJ) {
 #pragma unroll
                     for (int v = 0; v < V; ++v) st[v] = fmaf(av[i][v], st[v], bv[i][v]);
-                    store<T, V>(static_cast<T*>(a.h) + o, st);
+                    store<T, V>(static_cast<T*>(a.h) + at, st);
                 } else {
-                    float before[V], dg[V], dx[V];
-                    if (leaving >= 0) {
+                    float before[V], gv[V], xv[V], dg[V], dx[V];
+                    kg[i].get(gv);
+                    kx[i].get(xv);
+                    kh[i].get(before);
+                    if (leaving >= 0)
                         load_state<V>(a.state0 != nullptr ? a.state0 + leaving * a.d + c : nullptr, before);
-                    } else {
-#pragma unroll
-                        for (int v = 0; v < V; ++v) before[v] = kh[i].get(v);
-                    }
 #pragma unroll
                     for (int v = 0; v < V; ++v) {
                         float a2, cv;
-                        gate<GATE>(kg[i].get(v), a2, cv);
+                        gate<GATE>(gv[v], a2, cv);
                         const float lam = bv[i][v] + st[v];
                         dx[v] = comp ? lam * cv : lam;
-                        float da = lam * (comp ? before[v] - kx[i].get(v) : before[v]);
+                        float da = lam * (comp ? before[v] - xv[v] : before[v]);
                         if constexpr (GATE == CHOL_GATE_LOG) da *= a2;
                         if constexpr (GATE == CHOL_GATE_LOGIT) da *= a2 * cv;
                         dg[v] = da;
                         st[v] = av[i][v] * lam;
                     }
-                    store<T, V>(static_cast<T*>(a.adj_g) + o, dg);
-                    store<T, V>(static_cast<T*>(a.adj_x) + o, dx);
+                    store<T, V>(static_cast<T*>(a.adj_g) + at, dg);
+                    store<T, V>(static_cast<T*>(a.adj_x) + at, dx);
                 }
                 if (leaving >= 0 && state_out != nullptr) store_state<V>(state_out + leaving * a.d + c, st);
             }
+            parity ^= (uint32_t)buf;
             buf ^= 1;
         }
         if constexpr (PACKED) {
@@ -418,6 +481,7 @@ linrec_tile_kernel(const LinrecArgs a, const bool comp, const int64_t blocks, co
                 }
         }
     }
+    if (cs > 1) cluster_meet();  // no block leaves while another may write to it
 }
 
 // A few steps (one, in serving): a thread walks V channels by itself.
@@ -438,36 +502,32 @@ linrec_step_kernel(const LinrecArgs a, const bool comp) {
             Raw<T, V> rg, rx;
             rg.load(g + t * a.g_ts, true);
             rx.load(x + t * a.x_ts, !ADJ || comp);
+            float gv[V], xv[V], av[V], cv[V];
+            rg.get(gv);
+            rx.get(xv);
+#pragma unroll
+            for (int v = 0; v < V; ++v) gate<GATE>(gv[v], av[v], cv[v]);
             if constexpr (!ADJ) {
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    float av, cv;
-                    gate<GATE>(rg.get(v), av, cv);
-                    st[v] = fmaf(av, st[v], comp ? cv * rx.get(v) : rx.get(v));
-                }
+                for (int v = 0; v < V; ++v) st[v] = fmaf(av[v], st[v], comp ? cv[v] * xv[v] : xv[v]);
                 store<T, V>(static_cast<T*>(a.h) + o, st);
             } else {
                 Raw<T, V> rd, rh;
                 rd.load(static_cast<const T*>(a.adj_h) + b * a.dh_bs + t * a.dh_ts + c, true);
                 rh.load(static_cast<const T*>(a.h) + o - a.d, t > 0);
-                float before[V], dg[V], dx[V];
-                if (t > 0) {
-#pragma unroll
-                    for (int v = 0; v < V; ++v) before[v] = rh.get(v);
-                } else {
-                    load_state<V>(a.state0 != nullptr ? a.state0 + b * a.d + c : nullptr, before);
-                }
+                float before[V], dhv[V], dg[V], dx[V];
+                rd.get(dhv);
+                rh.get(before);
+                if (t == 0) load_state<V>(a.state0 != nullptr ? a.state0 + b * a.d + c : nullptr, before);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    float av, cv;
-                    gate<GATE>(rg.get(v), av, cv);
-                    const float lam = rd.get(v) + st[v];
-                    dx[v] = comp ? lam * cv : lam;
-                    float da = lam * (comp ? before[v] - rx.get(v) : before[v]);
-                    if constexpr (GATE == CHOL_GATE_LOG) da *= av;
-                    if constexpr (GATE == CHOL_GATE_LOGIT) da *= av * cv;
+                    const float lam = dhv[v] + st[v];
+                    dx[v] = comp ? lam * cv[v] : lam;
+                    float da = lam * (comp ? before[v] - xv[v] : before[v]);
+                    if constexpr (GATE == CHOL_GATE_LOG) da *= av[v];
+                    if constexpr (GATE == CHOL_GATE_LOGIT) da *= av[v] * cv[v];
                     dg[v] = da;
-                    st[v] = av * lam;
+                    st[v] = av[v] * lam;
                 }
                 store<T, V>(static_cast<T*>(a.adj_g) + o, dg);
                 store<T, V>(static_cast<T*>(a.adj_x) + o, dx);
@@ -488,7 +548,7 @@ struct Grid {
 inline Grid grid_of(const LinrecArgs& a, int C, int L) {
     Grid q;
     q.blocks = (a.d + C - 1) / C;
-    const int64_t total = a.batch * q.blocks, slots = 2 * (int64_t)device_sm_count();
+    const int64_t total = a.batch * q.blocks, slots = CHOL_LR_OCC * (int64_t)device_sm_count();
     const int64_t tiles = (a.time + L - 1) / L;
     q.cs = 1;
     while (q.cs < kMaxCluster && total * q.cs * 2 <= slots && q.cs < tiles) q.cs *= 2;
@@ -539,7 +599,7 @@ cudaError_t launch(const LinrecArgs& a, bool comp, bool vec, cudaStream_t stream
     if (a.batch * ((a.d + 8 * V - 1) / (8 * V)) * kMaxCluster < device_sm_count() &&
         a.time > kThreads / 8 * LS * kMaxCluster)
         return launch_any<T, V, 2, LS, GATE, ADJ>(a, comp, stream);
-    return launch_any<T, V, 8, LS, GATE, ADJ>(a, comp, stream);
+    return launch_any<T, CHOL_LR_V, CHOL_LR_CX, ADJ ? CHOL_LR_LSA : CHOL_LR_LSF, GATE, ADJ>(a, comp, stream);
 }
 
 }  // namespace linrec_detail
