@@ -59,6 +59,69 @@ __device__ __forceinline__ float rcp_fast(float x) {
     return y;
 }
 
+// d = a b + c, a b and a + b on V floats, two to an instruction (each rounded
+// as the scalar operation is).
+template <int V>
+__device__ __forceinline__ void fma_v(float (&d)[V], const float (&a)[V], const float (&b)[V],
+                                      const float (&c)[V]) {
+    if constexpr (V == 1) {
+        d[0] = fmaf(a[0], b[0], c[0]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i += 2)
+            asm("{\n\t.reg .b64 x, y, z;\n\t"
+                "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+                "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+                : "=f"(d[i]), "=f"(d[i + 1])
+                : "f"(a[i]), "f"(a[i + 1]), "f"(b[i]), "f"(b[i + 1]), "f"(c[i]), "f"(c[i + 1]));
+    }
+}
+template <int V>
+__device__ __forceinline__ void mul_v(float (&d)[V], const float (&a)[V], const float (&b)[V]) {
+    if constexpr (V == 1) {
+        d[0] = __fmul_rn(a[0], b[0]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i += 2)
+            asm("{\n\t.reg .b64 x, y;\n\t"
+                "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+                "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+                : "=f"(d[i]), "=f"(d[i + 1])
+                : "f"(a[i]), "f"(a[i + 1]), "f"(b[i]), "f"(b[i + 1]));
+    }
+}
+template <int V>
+__device__ __forceinline__ void add_v(float (&d)[V], const float (&a)[V], const float (&b)[V]) {
+    if constexpr (V == 1) {
+        d[0] = __fadd_rn(a[0], b[0]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i += 2)
+            asm("{\n\t.reg .b64 x, y;\n\t"
+                "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+                "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+                : "=f"(d[i]), "=f"(d[i + 1])
+                : "f"(a[i]), "f"(a[i + 1]), "f"(b[i]), "f"(b[i + 1]));
+    }
+}
+template <int V> __device__ __forceinline__ void fill_v(float (&d)[V], float x) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) d[i] = x;
+}
+// x d
+template <int V> __device__ __forceinline__ void scale_v(float (&d)[V], const float (&a)[V], float x) {
+    float k[V];
+    fill_v<V>(k, x);
+    mul_v<V>(d, a, k);
+}
+// a - b, as a + b (-1) exactly
+template <int V>
+__device__ __forceinline__ void sub_v(float (&d)[V], const float (&a)[V], const float (&b)[V]) {
+    float k[V];
+    fill_v<V>(k, -1.0f);
+    fma_v<V>(d, b, k, a);
+}
+
 // |x| as an unsigned integer: ordered as the numbers are, with infinity above
 // them and NaN above that, so that an integer maximum keeps a NaN and does
 // not depend on the order of its operands.
