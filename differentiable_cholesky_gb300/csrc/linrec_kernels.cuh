@@ -28,6 +28,9 @@
 // a_t lambda_t:  lambda_t = adj_h_t + carry_{t+1}.
 #pragma once
 
+#include <algorithm>
+#include <initializer_list>
+
 #include "learn.cuh"
 #include "learn.h"
 
@@ -275,6 +278,7 @@ __device__ __forceinline__ bool wait_maps(uint64_t* bar, uint32_t parity) {
 struct Marks {
     int* enter;
     int* leave;
+    int* any;  // whether there is one
 };
 
 // Marks of a tile whose steps are [lo, hi) of the time axis, by one warp;
@@ -284,6 +288,7 @@ template <int L, bool ADJ, typename F>
 __device__ __forceinline__ void mark(const LinrecArgs& a, int64_t lo, int64_t hi, Marks m, F row_of) {
     const int lane = threadIdx.x % 32;
     for (int i = lane; i < L; i += 32) m.enter[i] = m.leave[i] = -1;
+    if (lane == 0) *m.any = 0;
     __syncwarp();
     if (lo >= hi) return;
     // the first j with offsets[j] >= lo, 32 probes at a time
@@ -303,8 +308,8 @@ __device__ __forceinline__ void mark(const LinrecArgs& a, int64_t lo, int64_t hi
         if (o > hi) break;
         int* first = ADJ ? m.leave : m.enter;
         int* last = ADJ ? m.enter : m.leave;
-        if (o >= lo && o < hi && after > o) first[row_of(o)] = (int)j;
-        if (o - 1 >= lo && o - 1 < hi && before < o) last[row_of(o - 1)] = (int)j - 1;
+        if (o >= lo && o < hi && after > o) first[row_of(o)] = (int)j, *m.any = 1;
+        if (o - 1 >= lo && o - 1 < hi && before < o) last[row_of(o - 1)] = (int)j - 1, *m.any = 1;
     }
 }
 
@@ -323,7 +328,7 @@ linrec_tile_kernel(const LinrecArgs a, const bool comp, const int64_t blocks, co
     __shared__ float2 tile_map[2][kMost][C];
     __shared__ __align__(16) float warp_state[kWarps][C];
     __shared__ int warp_cut[kWarps], tile_cut[2][kMost];
-    __shared__ int marks[PACKED ? 2 : 1][2][PACKED ? L : 1];
+    __shared__ int marks[PACKED ? 2 : 1][2][PACKED ? L : 1], marked[2];
     __shared__ uint64_t arrived[2];  // the maps of a round, by its parity
 
     using Held = Hold<T, V, VEC>;
@@ -353,7 +358,7 @@ linrec_tile_kernel(const LinrecArgs a, const bool comp, const int64_t blocks, co
     // marks of the block's tile that starts at step u, by one warp
     auto mark_tile = [&](int64_t u, int at) {
         const int64_t last = min(u + L, U);
-        mark<L, ADJ>(a, ADJ ? U - last : u, ADJ ? U - u : last, {marks[at][0], marks[at][1]},
+        mark<L, ADJ>(a, ADJ ? U - last : u, ADJ ? U - u : last, {marks[at][0], marks[at][1], &marked[at]},
                      [&](int64_t t) { return (int)((ADJ ? U - 1 - t : t) - u); });
     };
     if (threadIdx.x == 0) {
@@ -448,12 +453,14 @@ linrec_tile_kernel(const LinrecArgs a, const bool comp, const int64_t blocks, co
                 }
             };
             int *enter = nullptr, *leave = nullptr;
+            bool some = false;  // a sequence begins or ends in this tile
             if constexpr (PACKED) {
                 enter = marks[buf][0], leave = marks[buf][1];
                 if (round == 0) {  // those of later tiles are made while maps are exchanged
                     if (warp == kWarps - 1) mark_tile(u0 - row0, buf);
                     __syncthreads();
                 }
+                some = marked[buf];
             }
             // a thread's steps to one map; a and what the steps add are kept
             float av[LS][V], bv[LS][V], A[V], H[V];
@@ -463,7 +470,7 @@ linrec_tile_kernel(const LinrecArgs a, const bool comp, const int64_t blocks, co
 #pragma unroll
             for (int i = 0; i < LS; ++i) {
                 if constexpr (PACKED) {
-                    const int s = enter[row0 + i];
+                    const int s = some ? enter[row0 + i] : -1;
                     if (s >= 0) {
                         cut = true;
                         load_state<V, STRIDE>(state_in != nullptr ? state_in + s * a.d + c : nullptr, chans, H);
@@ -580,9 +587,9 @@ linrec_tile_kernel(const LinrecArgs a, const bool comp, const int64_t blocks, co
                 if (i >= n) break;
                 int64_t leaving = -1;
                 if constexpr (PACKED) {
-                    const int e = enter[row0 + i];
+                    const int e = some ? enter[row0 + i] : -1;
                     if (e >= 0) load_state<V, STRIDE>(state_in != nullptr ? state_in + e * a.d + c : nullptr, chans, st);
-                    leaving = leave[row0 + i];
+                    if (some) leaving = leave[row0 + i];
                 } else {
                     if (u0 + i == U - 1) leaving = b;
                 }
@@ -677,62 +684,123 @@ linrec_step_kernel(const LinrecArgs a, const bool comp) {
     }
 }
 
+// One layout of a tile: launches, and what they would cost.
 template <typename T, int V, bool VEC, int CX, int LS, int GATE, bool ADJ, bool PACKED>
-cudaError_t launch_tile(const LinrecArgs& a, bool comp, cudaStream_t stream) {
-    constexpr auto kern = linrec_tile_kernel<T, V, VEC, CX, LS, GATE, ADJ, PACKED>;
-    constexpr int bytes = Hold<T, V, VEC>::ring_bytes(LS, ADJ), L = kThreads / CX * LS;
-    static std::atomic<uint64_t> set{0};
-    cudaError_t e = once_per_device(set, [&] {
-        const cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        return r != cudaSuccess
-                   ? r : cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    });
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute at[1];
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = bytes;
-    cfg.stream = stream;
-    cfg.attrs = at;
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    auto with = [&](int cs, unsigned clusters) {
-        cfg.gridDim = dim3(clusters * cs);
-        at[0].val.clusterDim.x = cs;
-        cfg.numAttrs = cs > 1 ? 1 : 0;
+struct Tile {
+    static constexpr auto kern = linrec_tile_kernel<T, V, VEC, CX, LS, GATE, ADJ, PACKED>;
+    static constexpr int kBytes = Hold<T, V, VEC>::ring_bytes(LS, ADJ), L = kThreads / CX * LS;
+    static constexpr int kMost = max_cluster_of<PACKED>::value;
+
+    static cudaError_t allow() {
+        static std::atomic<uint64_t> set{0};
+        return once_per_device(set, [&] {
+            const cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+            return r != cudaSuccess
+                       ? r : cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        });
+    }
+    static int64_t blocks(const LinrecArgs& a) { return (a.d + CX * V - 1) / (CX * V); }
+
+    struct Config {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute at[1];
+        Config(int cs, unsigned clusters, cudaStream_t stream) {
+            cfg.gridDim = dim3(clusters * cs);
+            cfg.blockDim = dim3(kThreads);
+            cfg.dynamicSmemBytes = kBytes;
+            cfg.stream = stream;
+            cfg.attrs = at;
+            cfg.numAttrs = cs > 1 ? 1 : 0;
+            at[0].id = cudaLaunchAttributeClusterDimension;
+            at[0].val.clusterDim.x = cs;
+            at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        }
     };
-    // Blocks of each cluster: all clusters take waves(cs) turns on the device,
-    // each of ceil(tiles / cs) rounds; a round that has to meet takes about a
-    // quarter longer (bf16 forward, 2048 channels: 3.1 us against 2.4 us).
-    const int64_t blocks = (a.d + CX * V - 1) / (CX * V), total = a.batch * blocks;
-    const int64_t tiles = (a.time + L - 1) / L;
-    constexpr int kMost = max_cluster_of<PACKED>::value;
-    static PerDeviceInt active[kMost + 1];
-    int best = 1;
-    double least = 0.0;
-    for (int cs = 1; cs <= kMost && (cs == 1 || cs <= tiles); ++cs) {
-        const int n = cs == 1 ? 2 * device_sm_count() : active[cs].get([&] {
-            int clusters = 0;
-            with(cs, 1);
-            if (cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg) != cudaSuccess) {
+
+    // Clusters of cs blocks that the device runs at once.
+    static int active(int cs) {
+        static PerDeviceInt cache[kMost + 1];
+        if (cs == 1) return 2 * device_sm_count();
+        return cache[cs].get([&] {
+            int n = 0;
+            Config c(cs, 1, nullptr);
+            if (cudaOccupancyMaxActiveClusters(&n, kern, &c.cfg) != cudaSuccess) {
                 cudaGetLastError();
                 return 0;
             }
-            return clusters;
+            return n;
         });
-        if (n <= 0) continue;
-        const double cost = (double)((total + n - 1) / n) * (double)((tiles + cs - 1) / cs) *
-                            (cs > 1 ? 1.25 : 1.0);
-        if (cs == 1 || cost < least) best = cs, least = cost;
     }
-    with(best, (unsigned)std::min<int64_t>(total, 1 << 24));
-    return cudaLaunchKernelEx(&cfg, kern, a, comp, blocks, best);
+
+    // The best cluster and its cost: every cluster takes `waves` turns on the
+    // device, each of ceil(tiles / cs) rounds.  A round that has to meet takes
+    // about a quarter longer (bf16 forward, 2048 channels: 3.1 us against 2.4).
+    static double cost(const LinrecArgs& a, int* best) {
+        const int64_t total = a.batch * blocks(a), tiles = (a.time + L - 1) / L;
+        double least = 0.0;
+        *best = 1;
+        for (int cs = 1; cs <= kMost && (cs == 1 || cs <= tiles); ++cs) {
+            const int n = active(cs);
+            if (n <= 0) continue;
+            const double c = (double)((total + n - 1) / n) * (double)((tiles + cs - 1) / cs) *
+                             (cs > 1 ? 1.25 : 1.0);
+            if (cs == 1 || c < least) *best = cs, least = c;
+        }
+        return least;
+    }
+
+    static cudaError_t run(const LinrecArgs& a, bool comp, int cs, cudaStream_t stream) {
+        Config c(cs, (unsigned)std::min<int64_t>(a.batch * blocks(a), 1 << 24), stream);
+        return cudaLaunchKernelEx(&c.cfg, kern, a, comp, blocks(a), cs);
+    }
+};
+
+// Runs the cheapest of several layouts of the same number of elements.
+// `weight` is what a tile of the layout takes, relative to the first.
+struct Weighed {
+    double weight;
+};
+template <typename First, typename... Rest>
+cudaError_t run_cheapest(const LinrecArgs& a, bool comp, cudaStream_t stream,
+                         std::initializer_list<Weighed> weights) {
+    double least = 0.0;
+    int pick = -1, size = 1, k = 0;
+    cudaError_t e = cudaSuccess;
+    auto look = [&](auto tile) {
+        using Tl = decltype(tile);
+        const cudaError_t r = Tl::allow();
+        if (r != cudaSuccess) { e = r; return; }
+        int cs = 1;
+        const double c = Tl::cost(a, &cs) * weights.begin()[k].weight;
+        if (pick < 0 || c < least) pick = k, least = c, size = cs;
+        ++k;
+    };
+    look(First{});
+    (look(Rest{}), ...);
+    if (e != cudaSuccess) return e;
+    k = 0;
+    auto go = [&](auto tile) {
+        if (k++ == pick) e = decltype(tile)::run(a, comp, size, stream);
+    };
+    go(First{});
+    (go(Rest{}), ...);
+    return e;
 }
 
-template <typename T, int V, bool VEC, int CX, int LS, int GATE, bool ADJ>
-cudaError_t launch_any(const LinrecArgs& a, bool comp, cudaStream_t stream) {
-    return a.offsets != nullptr ? launch_tile<T, V, VEC, CX, LS, GATE, ADJ, true>(a, comp, stream)
-                                : launch_tile<T, V, VEC, CX, LS, GATE, ADJ, false>(a, comp, stream);
+template <typename T, int GATE, bool ADJ, bool PACKED>
+cudaError_t launch_tiles(const LinrecArgs& a, bool comp, bool vec, cudaStream_t stream) {
+    constexpr int V = 16 / (int)sizeof(T), LS = ADJ ? 2 : 4;
+    // rows of 64 channels (128 bytes of 16-bit types), 32 or 16; the narrower
+    // ones exchange more within a warp, and pay where there are few channels
+    if (vec)
+        return run_cheapest<Tile<T, V, true, 8, LS, GATE, ADJ, PACKED>,
+                            Tile<T, V, true, 4, LS, GATE, ADJ, PACKED>,
+                            Tile<T, V, true, 2, LS, GATE, ADJ, PACKED>>(a, comp, stream,
+                                                                       {{1.0}, {ADJ ? 1.25 : 1.15}, {ADJ ? 1.5 : 1.35}});
+    return run_cheapest<Tile<T, 2, false, 32, 2 * LS, GATE, ADJ, PACKED>,
+                        Tile<T, 2, false, 16, 2 * LS, GATE, ADJ, PACKED>,
+                        Tile<T, 2, false, 8, 2 * LS, GATE, ADJ, PACKED>>(a, comp, stream,
+                                                                        {{1.0}, {1.1}, {1.2}});
 }
 
 // Steps that a thread walks by itself: up to here the chain of dependent
@@ -741,7 +809,7 @@ constexpr int64_t kFewSteps = 8;
 
 template <typename T, int GATE, bool ADJ>
 cudaError_t launch(const LinrecArgs& a, bool comp, bool vec, cudaStream_t stream) {
-    constexpr int V = 16 / (int)sizeof(T), LS = ADJ ? 2 : 4;
+    constexpr int V = 16 / (int)sizeof(T);
     if (a.time <= kFewSteps && a.offsets == nullptr) {
         const int64_t total = a.batch * ((a.d + (vec ? V : 1) - 1) / (vec ? V : 1));
         const unsigned grid = (unsigned)std::min<int64_t>((total + 127) / 128, 1 << 24);
@@ -749,12 +817,8 @@ cudaError_t launch(const LinrecArgs& a, bool comp, bool vec, cudaStream_t stream
         else linrec_step_kernel<T, 1, GATE, ADJ><<<grid, 128, 0, stream>>>(a, comp);
         return cudaGetLastError();
     }
-    if (!vec) return launch_any<T, 2, false, 32, 2 * LS, GATE, ADJ>(a, comp, stream);
-    // 128-byte rows of a channel block; 32-byte ones, and longer tiles, where
-    // the wider blocks would leave most SMs idle
-    if (a.batch * ((a.d + 8 * V - 1) / (8 * V)) * 8 < device_sm_count() && a.time > kThreads * LS)
-        return launch_any<T, V, true, 2, LS, GATE, ADJ>(a, comp, stream);
-    return launch_any<T, V, true, 8, LS, GATE, ADJ>(a, comp, stream);
+    return a.offsets != nullptr ? launch_tiles<T, GATE, ADJ, true>(a, comp, vec, stream)
+                                : launch_tiles<T, GATE, ADJ, false>(a, comp, vec, stream);
 }
 
 }  // namespace linrec_detail
