@@ -5,17 +5,26 @@
 //   adj_in = rstd (u - n mean(u n)) + adj_r,   adj_w = sum over rows of adj_y n
 //
 // Sums are float32; r is rounded only when it is written, y and the 8-bit
-// scales come from the unrounded r.
+// scales come from the unrounded r.  All of it is bound by memory: each row is
+// read once into registers, reduced over its threads, and written.  Three
+// forms of each direction:
+//   pipe: rows whose arrays are all vector-aligned, from 256 columns: a block
+//         keeps several rows on their way to shared memory (bulk copies that
+//         an mbarrier counts) while it works on one, so that loads never stop;
+//   row:  any alignment, up to 8192 columns: a row's threads take single
+//         elements side by side;
+//   loop: any width: a block goes over its row two or three times.
 
 #include <algorithm>
 
+#include "checks.h"
 #include "learn.cuh"
 #include "learn.h"
 
 namespace chol {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;  // of the loop kernels
 
 enum OutKind { OUT_MODEL, OUT_E4M3, OUT_I8 };
 
@@ -32,6 +41,27 @@ template <int OUT> __device__ __forceinline__ float scale_of(uint32_t top) {
 }
 __device__ __forceinline__ float inverse_of(float scale) {
     return scale > 0.0f ? __frcp_rn(scale) : 0.0f;
+}
+
+// Eight codes, 8-byte aligned.
+template <int OUT>
+__device__ __forceinline__ void store_codes(uint8_t* p, const float (&v)[8], float inv) {
+    uint32_t w[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if constexpr (OUT == OUT_E4M3) {
+            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * h] * inv, v[4 * h + 1] * inv),
+                                                         __NV_SATFINITE, __NV_E4M3);
+            const uint32_t hi = __nv_cvt_float2_to_fp8x2(
+                make_float2(v[4 * h + 2] * inv, v[4 * h + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+            w[h] = lo | hi << 16;
+        } else {
+            w[h] = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[h] |= (uint32_t)to_code8<OUT>(v[4 * h + i] * inv) << (8 * i);
+        }
+    }
+    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
 }
 
 // Any d and any alignment: a block goes over its row two or three times (sum
@@ -111,10 +141,11 @@ __global__ void __launch_bounds__(kThreads) rms_norm_loop_kernel(RmsArgs a) {
     }
 }
 
-// Rows of the adjoint that one partial sum of adj_w covers: few enough
-// partial sums that writing and adding them stays small beside the rows.
-inline int64_t adj_w_parts(int64_t rows) {
-    return std::max<int64_t>(1, std::min<int64_t>(rows, (int64_t)device_sm_count() * 2));
+// Partial sums of adj_w, each over every `parts`-th row: what keeps the device
+// busy with blocks of a row's threads, and is small beside the rows.
+inline int64_t adj_w_parts(int64_t rows, int64_t d) {
+    const int64_t per_sm = std::max<int64_t>(2, std::min<int64_t>(16, 8192 / d));
+    return std::max<int64_t>(1, std::min<int64_t>(rows, device_sm_count() * per_sm));
 }
 
 // One block per part: rows part, part + parts, ...; their adj_y n summed into
@@ -149,41 +180,623 @@ __global__ void __launch_bounds__(kThreads) rms_norm_adj_loop_kernel(RmsAdjArgs 
     }
 }
 
-// adj_w[j] = sum over parts, in order.
+// adj_w[j] = sum over the parts: a block takes 32 columns, each of its 32 warps
+// every 32nd part, and the warps' sums are added in order.
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(1024)
 column_sum_kernel(const float* __restrict__ work, int64_t parts, int64_t d, T* __restrict__ out) {
-    for (int64_t j = (int64_t)blockIdx.x * kThreads + threadIdx.x; j < d;
-         j += (int64_t)gridDim.x * kThreads) {
-        float s = 0.0f;
-        for (int64_t p = 0; p < parts; ++p) s += work[p * d + j];
-        out[j] = from_f32<T>(s);
+    __shared__ float sums[32][33];
+    pdl_wait();
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int64_t j = (int64_t)blockIdx.x * 32 + lane;
+    float s = 0.0f;
+    if (j < d) {
+#pragma unroll 8
+        for (int64_t p = warp; p < parts; p += 32) s += work[p * d + j];
     }
+    sums[warp][lane] = s;
+    __syncthreads();
+    if (warp != 0 || j >= d) return;
+    s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 32; ++w) s += sums[w][lane];
+    out[j] = from_f32<T>(s);
+}
+
+// ---------------------------------------------------------------------------
+// A row's values in registers
+// ---------------------------------------------------------------------------
+
+// Eight consecutive elements, 16 or 32 bytes of memory aligned to that.
+template <typename T> struct Eight {
+    uint32_t w[2 * sizeof(T)];
+    __device__ __forceinline__ void load_shared(const void* p) {
+        const uint4* q = static_cast<const uint4*>(p);
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+            const uint4 v = q[i];
+            w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+        }
+    }
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) * 2; ++i) {
+            if constexpr (sizeof(T) == 4) f[i] = __uint_as_float(w[i]);
+            else unpack2<T>(w[i], f[2 * i], f[2 * i + 1]);
+        }
+    }
+    __device__ __forceinline__ void set(const float (&f)[8]) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) * 2; ++i) {
+            if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(f[i]);
+            else w[i] = pack2<T>(f[2 * i], f[2 * i + 1]);
+        }
+    }
+    __device__ __forceinline__ void load(const T* p) {
+        if constexpr (sizeof(T) == 4)
+            asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
+                           "=r"(w[6]), "=r"(w[7]) : "l"(p));
+        else
+            asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
+    }
+    __device__ __forceinline__ void store(T* p) const {
+        if constexpr (sizeof(T) == 4)
+            asm volatile("st.global.v8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::
+                             "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]),
+                             "r"(w[6]), "r"(w[7]), "l"(p) : "memory");
+        else
+            asm volatile("st.global.v4.b32 [%4], {%0, %1, %2, %3};" ::
+                             "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "l"(p) : "memory");
+    }
+};
+
+// Sum (or largest bits) over the `warps` warps of one row; `tmp` holds a word
+// for each and is written again only after another barrier of the block.
+__device__ __forceinline__ float row_sum(float x, float* tmp, int warp, int warps) {
+    x = warp_sum(x);
+    if (warps == 1) return x;
+    const int lane = threadIdx.x % 32;
+    if (lane == 0) tmp[warp] = x;
+    __syncthreads();
+    return warp_sum(lane < warps ? tmp[lane] : 0.0f);
+}
+__device__ __forceinline__ uint32_t row_max(uint32_t x, uint32_t* tmp, int warp, int warps) {
+    x = warp_max(x);
+    if (warps == 1) return x;
+    const int lane = threadIdx.x % 32;
+    if (lane == 0) tmp[warp] = x;
+    __syncthreads();
+    return warp_max(lane < warps ? tmp[lane] : 0u);
+}
+
+// ---------------------------------------------------------------------------
+// pipe: one row at a time, the next ones on their way
+// ---------------------------------------------------------------------------
+constexpr int kMaxStages = 6;
+
+struct Pipe {
+    int threads, stages;
+    unsigned blocks;
+    size_t bytes;
+};
+
+// The copies of a block's rows into a ring of stages.  ROWS arrays of
+// `bytes[i]` a row; stage s begins at ring + s * stage_bytes.
+template <int ARRAYS>
+struct RowCopies {
+    const char* at[ARRAYS];   // the array's row `first`
+    int64_t step[ARRAYS];     // bytes between rows
+    uint32_t bytes[ARRAYS];
+    uint32_t total;           // of a stage
+    __device__ __forceinline__ void issue(char* stage, uint64_t* bar, int64_t row) const {
+        mbar_arrive_expect_tx(bar, total);
+        uint32_t off = 0;
+#pragma unroll
+        for (int i = 0; i < ARRAYS; ++i) {
+            if (bytes[i] > 0) bulk_load(stage + off, at[i] + row * step[i], bytes[i], bar);
+            off += bytes[i];
+        }
+    }
+};
+
+// Waits for a stage; after a wait that ran out, rows count as NaN.
+__device__ __forceinline__ float stage_ready(uint64_t* bar, uint32_t parity, bool& lost) {
+    lost = lost || !mbar_wait(bar, parity, 1u << 20);
+    return lost ? __int_as_float(0x7fffffff) : 0.0f;
+}
+
+// K vectors of eight columns a thread.
+template <typename T, typename R, int OUT, int K>
+__global__ void __launch_bounds__(512) rms_norm_pipe_kernel(const RmsArgs a, const int stages) {
+    extern __shared__ __align__(128) char ring[];
+    __shared__ uint64_t bars[kMaxStages];
+    __shared__ float tmp[2][32];
+    __shared__ uint32_t tmp_max[2][32];
+    const int d = (int)a.d, nt = blockDim.x, warp = threadIdx.x / 32, warps = nt / 32;
+    const bool has_res = a.res != nullptr;
+    RowCopies<2> copies;
+    copies.at[0] = static_cast<const char*>(a.x), copies.step[0] = a.ldx * (int64_t)sizeof(T);
+    copies.at[1] = static_cast<const char*>(a.res), copies.step[1] = a.ldr * (int64_t)sizeof(R);
+    copies.bytes[0] = d * (uint32_t)sizeof(T), copies.bytes[1] = has_res ? d * (uint32_t)sizeof(R) : 0;
+    copies.total = copies.bytes[0] + copies.bytes[1];
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) mbar_init(&bars[s], 1);
+        fence_mbar_init();
+        for (int s = 0; s < stages; ++s) {
+            const int64_t row = blockIdx.x + (int64_t)s * gridDim.x;
+            if (row < a.rows) copies.issue(ring + (size_t)s * copies.total, &bars[s], row);
+        }
+    }
+    Eight<T> w[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int j = (k * nt + threadIdx.x) * 8;
+        if (a.w != nullptr && j < d) w[k].load(static_cast<const T*>(a.w) + j);
+    }
+    __syncthreads();
+    int stage = 0, turn = 0;
+    uint32_t parity = 0;
+    bool lost = false;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+        const char* at = ring + (size_t)stage * copies.total;
+        const float poison = stage_ready(&bars[stage], parity, lost);
+        float v[K][8], ss = poison;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int j = (k * nt + threadIdx.x) * 8;
+            fill_v<8>(v[k], 0.0f);
+            if (j < d) {
+                Eight<T> q;
+                q.load_shared(at + j * sizeof(T));
+                q.get(v[k]);
+                if (has_res) {
+                    Eight<R> p;
+                    float f[8];
+                    p.load_shared(at + copies.bytes[0] + j * sizeof(R));
+                    p.get(f);
+                    add_v<8>(v[k], v[k], f);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss = fmaf(v[k][i], v[k][i], ss);
+        }
+        if (warps > 1) {
+            ss = row_sum(ss, tmp[turn], warp, warps);
+        } else {
+            ss = warp_sum(ss);
+            __syncwarp();
+        }
+        // every thread has its row in registers: the stage is free
+        if (threadIdx.x == 0) {
+            const int64_t next = row + (int64_t)stages * gridDim.x;
+            if (next < a.rows) copies.issue(ring + (size_t)stage * copies.total, &bars[stage], next);
+        }
+        if (++stage == stages) stage = 0, parity ^= 1;
+        const float rstd = rsqrtf(ss / (float)d + a.eps);
+        if (threadIdx.x == 0 && a.rstd != nullptr) a.rstd[row] = rstd;
+        uint32_t row_top = 0;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int j = (k * nt + threadIdx.x) * 8;
+            if (j < d && a.r != nullptr) {
+                Eight<R> p;
+                p.set(v[k]);
+                p.store(static_cast<R*>(a.r) + row * a.d + j);
+            }
+            scale_v<8>(v[k], v[k], rstd);
+            if (a.w != nullptr && j < d) {
+                float f[8];
+                w[k].get(f);
+                mul_v<8>(v[k], v[k], f);
+            }
+            if constexpr (OUT == OUT_MODEL) {
+                if (j < d) {
+                    Eight<T> q;
+                    q.set(v[k]);
+                    q.store(static_cast<T*>(a.y) + row * a.d + j);
+                }
+            } else {
+                uint32_t top = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) top = max(top, abs_bits(v[k][i]));
+                if (a.group == 0) {
+                    row_top = max(row_top, top);
+                } else {
+                    // 16 threads hold a group of 128 columns
+#pragma unroll
+                    for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    const float scale = scale_of<OUT>(top);
+                    if (j < d) {
+                        if (threadIdx.x % 16 == 0) a.scale[row * ((d + 127) / 128) + j / 128] = scale;
+                        store_codes<OUT>(static_cast<uint8_t*>(a.y) + row * a.d + j, v[k], inverse_of(scale));
+                    }
+                }
+            }
+        }
+        if constexpr (OUT != OUT_MODEL) {
+            if (a.group == 0) {
+                const float scale = scale_of<OUT>(row_max(row_top, tmp_max[turn], warp, warps));
+                if (threadIdx.x == 0) a.scale[row] = scale;
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    const int j = (k * nt + threadIdx.x) * 8;
+                    if (j < d)
+                        store_codes<OUT>(static_cast<uint8_t*>(a.y) + row * a.d + j, v[k], inverse_of(scale));
+                }
+            }
+        }
+    }
+}
+
+template <typename T, typename R, int K>
+__global__ void __launch_bounds__(512) rms_norm_adj_pipe_kernel(const RmsAdjArgs a, const int stages) {
+    extern __shared__ __align__(128) char ring[];
+    __shared__ uint64_t bars[kMaxStages];
+    __shared__ float tmp[2][32];
+    const int d = (int)a.d, nt = blockDim.x, warp = threadIdx.x / 32, warps = nt / 32;
+    const bool has_dr = a.adj_r != nullptr;
+    RowCopies<3> copies;
+    copies.at[0] = static_cast<const char*>(a.adj_y), copies.step[0] = a.ldy * (int64_t)sizeof(T);
+    copies.at[1] = static_cast<const char*>(a.r), copies.step[1] = a.ldr * (int64_t)sizeof(R);
+    copies.at[2] = static_cast<const char*>(a.adj_r), copies.step[2] = a.d * (int64_t)sizeof(R);
+    copies.bytes[0] = d * (uint32_t)sizeof(T), copies.bytes[1] = d * (uint32_t)sizeof(R);
+    copies.bytes[2] = has_dr ? copies.bytes[1] : 0;
+    copies.total = copies.bytes[0] + copies.bytes[1] + copies.bytes[2];
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) mbar_init(&bars[s], 1);
+        fence_mbar_init();
+        for (int s = 0; s < stages; ++s) {
+            const int64_t row = blockIdx.x + (int64_t)s * gridDim.x;
+            if (row < a.rows) copies.issue(ring + (size_t)s * copies.total, &bars[s], row);
+        }
+    }
+    Eight<T> w[K];
+    float dw[K][8];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int j = (k * nt + threadIdx.x) * 8;
+        if (a.w != nullptr && j < d) w[k].load(static_cast<const T*>(a.w) + j);
+        fill_v<8>(dw[k], 0.0f);
+    }
+    __syncthreads();
+    int stage = 0, turn = 0;
+    uint32_t parity = 0;
+    bool lost = false;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+        const char* at = ring + (size_t)stage * copies.total;
+        const float rstd = a.rstd[row];
+        float c = stage_ready(&bars[stage], parity, lost);
+        float u[K][8], n[K][8];
+        Eight<R> add[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int j = (k * nt + threadIdx.x) * 8;
+            if (j >= d) continue;
+            Eight<T> q;
+            q.load_shared(at + j * sizeof(T));
+            q.get(u[k]);
+            Eight<R> p;
+            p.load_shared(at + copies.bytes[0] + j * sizeof(R));
+            p.get(n[k]);
+            if (has_dr) add[k].load_shared(at + copies.bytes[0] + copies.bytes[1] + j * sizeof(R));
+            scale_v<8>(n[k], n[k], rstd);
+            fma_v<8>(dw[k], u[k], n[k], dw[k]);
+            if (a.w != nullptr) {
+                float f[8];
+                w[k].get(f);
+                mul_v<8>(u[k], u[k], f);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) c = fmaf(u[k][i], n[k][i], c);
+        }
+        if (warps > 1) {
+            c = row_sum(c, tmp[turn], warp, warps);
+        } else {
+            c = warp_sum(c);
+            __syncwarp();
+        }
+        if (threadIdx.x == 0) {
+            const int64_t next = row + (int64_t)stages * gridDim.x;
+            if (next < a.rows) copies.issue(ring + (size_t)stage * copies.total, &bars[stage], next);
+        }
+        if (++stage == stages) stage = 0, parity ^= 1;
+        c /= (float)d;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int j = (k * nt + threadIdx.x) * 8;
+            if (j >= d) continue;
+            // rstd (u - n c) + adj_r
+            float f[8], s[8];
+            fill_v<8>(f, -c);
+            fma_v<8>(u[k], n[k], f, u[k]);
+            fill_v<8>(s, rstd);
+            fill_v<8>(f, 0.0f);
+            if (has_dr) add[k].get(f);
+            fma_v<8>(u[k], u[k], s, f);
+            if (a.adj_in != nullptr) {
+                Eight<R> p;
+                p.set(u[k]);
+                p.store(static_cast<R*>(a.adj_in) + row * a.d + j);
+            }
+            if (a.adj_x != nullptr) {
+                Eight<T> q;
+                q.set(u[k]);
+                q.store(static_cast<T*>(a.adj_x) + row * a.d + j);
+            }
+        }
+    }
+    if (a.adj_w == nullptr) return;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int j = (k * nt + threadIdx.x) * 8;
+        if (j >= d) continue;
+        float* part = a.work + (int64_t)blockIdx.x * a.d + j;
+#pragma unroll
+        for (int i = 0; i < 8; i += 4)
+            *reinterpret_cast<float4*>(part + i) =
+                make_float4(dw[k][i], dw[k][i + 1], dw[k][i + 2], dw[k][i + 3]);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// row: single elements side by side, E of them a thread
+// ---------------------------------------------------------------------------
+template <typename T, typename R, int OUT, int E>
+__global__ void __launch_bounds__(1024) rms_norm_row_kernel(const RmsArgs a) {
+    // blockDim.x threads a row, blockDim.y rows
+    extern __shared__ uint32_t row_smem[];  // per row: 32 words for sums, then one per group
+    const int d = (int)a.d, nt = blockDim.x, warp = threadIdx.x / 32, warps = nt / 32;
+    const int groups = a.group != 0 ? (d + 127) / 128 : 1;
+    uint32_t* mine = row_smem + threadIdx.y * (32 + groups);
+    const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    const bool here = row < a.rows;
+    const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+    const R* res = static_cast<const R*>(a.res) + row * a.ldr;
+    float v[E], ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+        const int j = i * nt + threadIdx.x;
+        v[i] = here && j < d ? to_f32(x[j]) : 0.0f;
+    }
+    if (a.res != nullptr) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            const int j = i * nt + threadIdx.x;
+            if (here && j < d) v[i] += to_f32(res[j]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i) ss = fmaf(v[i], v[i], ss);
+    if constexpr (OUT != OUT_MODEL)
+        for (int g = threadIdx.x; g < groups; g += nt) mine[32 + g] = 0;
+    ss = row_sum(ss, reinterpret_cast<float*>(mine), warp, warps);
+    const float rstd = rsqrtf(ss / (float)d + a.eps);
+    if (here && threadIdx.x == 0 && a.rstd != nullptr) a.rstd[row] = rstd;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+        const int j = i * nt + threadIdx.x;
+        if (!here || j >= d) continue;
+        if (a.r != nullptr) static_cast<R*>(a.r)[row * a.d + j] = from_f32<R>(v[i]);
+        v[i] *= rstd;
+        if (a.w != nullptr) v[i] *= to_f32(static_cast<const T*>(a.w)[j]);
+        if constexpr (OUT == OUT_MODEL) static_cast<T*>(a.y)[row * a.d + j] = from_f32<T>(v[i]);
+    }
+    if constexpr (OUT != OUT_MODEL) {
+        // 32 columns side by side are a warp's, and of one group
+        if (warps == 1) __syncwarp();
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            const int j = i * nt + threadIdx.x, j0 = i * nt + warp * 32;
+            const uint32_t top = warp_max(j < d ? abs_bits(v[i]) : 0u);
+            if (threadIdx.x % 32 == 0 && j0 < d) atomicMax(mine + 32 + (a.group != 0 ? j0 / 128 : 0), top);
+        }
+        if (warps == 1) __syncwarp(); else __syncthreads();
+        for (int g = threadIdx.x; g < groups; g += nt)
+            if (here) a.scale[row * groups + g] = scale_of<OUT>(mine[32 + g]);
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            const int j = i * nt + threadIdx.x;
+            if (!here || j >= d) continue;
+            const float inv = inverse_of(scale_of<OUT>(mine[32 + (a.group != 0 ? j / 128 : 0)]));
+            static_cast<uint8_t*>(a.y)[row * a.d + j] = to_code8<OUT>(v[i] * inv);
+        }
+    }
+}
+
+// Row index blockIdx.x * blockDim.y + threadIdx.y of every `parts` rows.
+template <typename T, typename R, int E>
+__global__ void __launch_bounds__(1024) rms_norm_adj_row_kernel(const RmsAdjArgs a, const int64_t parts) {
+    __shared__ float tmp[2][32];
+    const int d = (int)a.d, nt = blockDim.x, warp = threadIdx.x / 32, warps = nt / 32;
+    const int64_t part = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    float dw[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) dw[i] = 0.0f;
+    int turn = 0;
+    // blockDim.y > 1 only with one warp a row, which needs no barrier
+    for (int64_t row = part; row < a.rows && part < parts; row += parts, turn ^= 1) {
+        const T* dy = static_cast<const T*>(a.adj_y) + row * a.ldy;
+        const R* r = static_cast<const R*>(a.r) + row * a.ldr;
+        const R* dr = static_cast<const R*>(a.adj_r) + row * a.d;
+        const float rstd = a.rstd[row];
+        float u[E], n[E], add[E], c = 0.0f;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            const int j = i * nt + threadIdx.x;
+            u[i] = j < d ? to_f32(dy[j]) : 0.0f;
+            n[i] = j < d ? to_f32(r[j]) : 0.0f;
+            add[i] = j < d && a.adj_r != nullptr ? to_f32(dr[j]) : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            const int j = i * nt + threadIdx.x;
+            n[i] *= rstd;
+            dw[i] = fmaf(u[i], n[i], dw[i]);
+            if (a.w != nullptr && j < d) u[i] *= to_f32(static_cast<const T*>(a.w)[j]);
+            c = fmaf(u[i], n[i], c);
+        }
+        c = row_sum(c, tmp[turn], warp, warps) / (float)d;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            const int j = i * nt + threadIdx.x;
+            if (j >= d) continue;
+            const float v = fmaf(rstd, u[i] - n[i] * c, add[i]);
+            if (a.adj_in != nullptr) static_cast<R*>(a.adj_in)[row * a.d + j] = from_f32<R>(v);
+            if (a.adj_x != nullptr) static_cast<T*>(a.adj_x)[row * a.d + j] = from_f32<T>(v);
+        }
+    }
+    if (a.adj_w == nullptr || part >= parts) return;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+        const int j = i * nt + threadIdx.x;
+        if (j < d) a.work[part * a.d + j] = dw[i];
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Choice
+// ---------------------------------------------------------------------------
+bool rows_aligned(const void* p, int64_t ld, size_t es) {
+    return p == nullptr || (aligned(p, 8 * es) && ld % 8 == 0);
+}
+
+// Threads and stages for rows of `vecs` vectors and `bytes` bytes to copy;
+// `per_sm` blocks share an SM's shared memory.  stages < 2: it does not fit.
+Pipe pipe_of(int64_t rows, int64_t vecs, int64_t bytes, int k, int64_t blocks) {
+    Pipe p = {};
+    p.threads = (int)((vecs + k * 32 - 1) / (k * 32)) * 32;
+    if (p.threads > 512) return p;
+    const int sms = device_sm_count();
+    p.blocks = (unsigned)std::min(rows, blocks);
+    const int64_t share = std::max<int64_t>(1, (p.blocks + sms - 1) / sms);
+    const int64_t fits = (216 * 1024 / share - 2048) / bytes;
+    p.stages = (int)std::min<int64_t>(fits, kMaxStages);
+    p.stages = (int)std::min<int64_t>(p.stages, std::max<int64_t>(2, (rows + p.blocks - 1) / p.blocks));
+    p.bytes = (size_t)p.stages * bytes;
+    return p;
+}
+
+template <typename K, typename A>
+cudaError_t launch_pipe(K kern, const Pipe& p, const A& a, std::atomic<uint64_t>& set, cudaStream_t stream) {
+    const cudaError_t e = allow_smem_once(kern, 224 * 1024, set);
+    if (e != cudaSuccess) return e;
+    kern<<<p.blocks, p.threads, p.bytes, stream>>>(a, p.stages);
+    return cudaGetLastError();
+}
+
+template <typename T, typename R, int OUT, int K>
+cudaError_t try_pipe(const RmsArgs& a, int64_t per_sm, bool* ran, cudaStream_t stream) {
+    static std::atomic<uint64_t> set{0};
+    const int64_t bytes = a.d * (int64_t)(sizeof(T) + (a.res != nullptr ? sizeof(R) : 0));
+    const Pipe p = pipe_of(a.rows, a.d / 8, bytes, K, device_sm_count() * per_sm);
+    *ran = p.stages >= 2;
+    if (!*ran) return cudaSuccess;
+    return launch_pipe(rms_norm_pipe_kernel<T, R, OUT, K>, p, a, set, stream);
+}
+
+template <typename T, typename R, int OUT, int E>
+cudaError_t launch_rows(const RmsArgs& a, cudaStream_t stream) {
+    const int nt = (int)((a.d + E * 32 - 1) / (E * 32)) * 32;
+    const int per = nt == 32 ? 4 : 1;  // rows of a block
+    const size_t groups = a.group != 0 ? (a.d + 127) / 128 : 1;
+    const int64_t blocks = (a.rows + per - 1) / per;
+    for (int64_t b = 0; b < blocks; b += 1 << 30) {  // (one launch but for over 2^30 rows)
+        RmsArgs q = a;
+        const int64_t from = b * per;
+        q.rows = std::min<int64_t>(a.rows - from, (int64_t)per << 30);
+        q.x = static_cast<const T*>(a.x) + from * a.ldx;
+        q.res = a.res != nullptr ? static_cast<const R*>(a.res) + from * a.ldr : nullptr;
+        q.y = static_cast<char*>(a.y) + from * a.d * (OUT == OUT_MODEL ? sizeof(T) : 1);
+        q.scale = a.scale != nullptr ? a.scale + from * groups : nullptr;
+        q.r = a.r != nullptr ? static_cast<R*>(a.r) + from * a.d : nullptr;
+        q.rstd = a.rstd != nullptr ? a.rstd + from : nullptr;
+        const unsigned grid = (unsigned)((q.rows + per - 1) / per);
+        rms_norm_row_kernel<T, R, OUT, E>
+            <<<grid, dim3(nt, per), (32 + groups) * per * sizeof(uint32_t), stream>>>(q);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+template <typename T, typename R, int OUT>
+cudaError_t launch_out(const RmsArgs& a, cudaStream_t stream) {
+    const size_t ys = OUT == OUT_MODEL ? sizeof(T) : 1;
+    const bool vec = a.d % 8 == 0 && a.d >= 256 && rows_aligned(a.x, a.ldx, sizeof(T)) &&
+                     rows_aligned(a.res, a.ldr, sizeof(R)) && rows_aligned(a.r, a.d, sizeof(R)) &&
+                     rows_aligned(a.w, 8, sizeof(T)) && aligned(a.y, 8 * ys);
+    if (vec) {
+        bool ran = false;
+        const int64_t per_sm = std::max<int64_t>(2, std::min<int64_t>(16, 8192 / a.d));
+        // one vector a thread where there are few rows or narrow ones
+        const bool few = a.rows <= device_sm_count() || a.d <= 2048;
+        cudaError_t e = cudaSuccess;
+        if (few) e = try_pipe<T, R, OUT, 1>(a, per_sm, &ran, stream);
+        if (!ran) e = try_pipe<T, R, OUT, 2>(a, per_sm, &ran, stream);
+        if (!ran) e = try_pipe<T, R, OUT, 4>(a, per_sm, &ran, stream);
+        if (ran) return e;
+    }
+    if (a.d <= 1024) return launch_rows<T, R, OUT, 4>(a, stream);
+    if (a.d <= 8192) return launch_rows<T, R, OUT, 8>(a, stream);
+    const unsigned blocks = (unsigned)std::min<int64_t>(a.rows, 1 << 20);
+    rms_norm_loop_kernel<T, R, OUT><<<blocks, kThreads, 0, stream>>>(a);
+    return cudaGetLastError();
 }
 
 template <typename T, typename R>
 cudaError_t launch_fwd(const RmsArgs& a, int32_t y_dtype, cudaStream_t stream) {
-    const unsigned blocks = (unsigned)std::min<int64_t>(a.rows, 1 << 20);
-    if (y_dtype == CHOL_E4M3)
-        rms_norm_loop_kernel<T, R, OUT_E4M3><<<blocks, kThreads, 0, stream>>>(a);
-    else if (y_dtype == CHOL_I8)
-        rms_norm_loop_kernel<T, R, OUT_I8><<<blocks, kThreads, 0, stream>>>(a);
-    else
-        rms_norm_loop_kernel<T, R, OUT_MODEL><<<blocks, kThreads, 0, stream>>>(a);
+    if (y_dtype == CHOL_E4M3) return launch_out<T, R, OUT_E4M3>(a, stream);
+    if (y_dtype == CHOL_I8) return launch_out<T, R, OUT_I8>(a, stream);
+    return launch_out<T, R, OUT_MODEL>(a, stream);
+}
+
+template <typename T, typename R, int K>
+cudaError_t try_adj_pipe(const RmsAdjArgs& a, int64_t parts, bool* ran, cudaStream_t stream) {
+    static std::atomic<uint64_t> set{0};
+    const int64_t bytes = a.d * (int64_t)(sizeof(T) + sizeof(R) * (a.adj_r != nullptr ? 2 : 1));
+    const Pipe p = pipe_of(a.rows, a.d / 8, bytes, K, parts);
+    *ran = p.stages >= 2;
+    if (!*ran) return cudaSuccess;
+    return launch_pipe(rms_norm_adj_pipe_kernel<T, R, K>, p, a, set, stream);
+}
+
+template <typename T, typename R, int E>
+cudaError_t launch_adj_rows(const RmsAdjArgs& a, int64_t parts, cudaStream_t stream) {
+    const int nt = (int)((a.d + E * 32 - 1) / (E * 32)) * 32;
+    const int per = nt == 32 ? 4 : 1;
+    const unsigned grid = (unsigned)((parts + per - 1) / per);
+    rms_norm_adj_row_kernel<T, R, E><<<grid, dim3(nt, per), 0, stream>>>(a, parts);
     return cudaGetLastError();
 }
 
 template <typename T, typename R>
 cudaError_t launch_adj(const RmsAdjArgs& a, cudaStream_t stream) {
-    const int64_t parts = adj_w_parts(a.rows);
-    const unsigned blocks = (unsigned)parts;
-    rms_norm_adj_loop_kernel<T, R><<<blocks, kThreads, 0, stream>>>(a);
-    cudaError_t e = cudaGetLastError();
+    const int64_t parts = adj_w_parts(a.rows, a.d);
+    const bool vec = a.d % 8 == 0 && a.d >= 256 && rows_aligned(a.adj_y, a.ldy, sizeof(T)) &&
+                     rows_aligned(a.r, a.ldr, sizeof(R)) && rows_aligned(a.adj_r, a.d, sizeof(R)) &&
+                     rows_aligned(a.adj_in, a.d, sizeof(R)) && rows_aligned(a.adj_x, a.d, sizeof(T)) &&
+                     rows_aligned(a.w, 8, sizeof(T));
+    cudaError_t e = cudaSuccess;
+    bool ran = false;
+    if (vec) {
+        if (a.d <= 4096) e = try_adj_pipe<T, R, 1>(a, parts, &ran, stream);
+        if (!ran && e == cudaSuccess) e = try_adj_pipe<T, R, 2>(a, parts, &ran, stream);
+    }
+    if (!ran) {
+        if (a.d <= 1024) {
+            e = launch_adj_rows<T, R, 4>(a, parts, stream);
+        } else if (a.d <= 8192) {
+            e = launch_adj_rows<T, R, 8>(a, parts, stream);
+        } else {
+            rms_norm_adj_loop_kernel<T, R><<<(unsigned)parts, kThreads, 0, stream>>>(a);
+            e = cudaGetLastError();
+        }
+    }
     if (e != cudaSuccess || a.adj_w == nullptr) return e;
-    const unsigned cols = (unsigned)((a.d + kThreads - 1) / kThreads);
-    column_sum_kernel<T><<<cols, kThreads, 0, stream>>>(a.work, parts, a.d,
-                                                        static_cast<T*>(a.adj_w));
-    return cudaGetLastError();
+    return launch_pdl(column_sum_kernel<T>, dim3((unsigned)((a.d + 31) / 32)), dim3(1024), 0, stream,
+                      static_cast<const float*>(a.work), parts, a.d, static_cast<T*>(a.adj_w));
 }
 
 }  // namespace
@@ -198,7 +811,7 @@ cudaError_t rms_norm(const RmsArgs& a, int32_t dtype, int32_t res_dtype, int32_t
 }
 
 size_t rms_norm_adj_workspace_bytes(int64_t rows, int64_t d) {
-    return rows <= 0 ? 0 : (size_t)adj_w_parts(rows) * (size_t)d * sizeof(float);
+    return rows <= 0 ? 0 : (size_t)adj_w_parts(rows, d) * (size_t)d * sizeof(float);
 }
 
 cudaError_t rms_norm_adj(const RmsAdjArgs& a, int32_t dtype, int32_t r_dtype,
