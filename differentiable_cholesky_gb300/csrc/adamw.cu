@@ -20,6 +20,7 @@
 #include <memory>
 #include <new>
 
+#include "checks.h"
 #include "learn.cuh"
 #include "learn.h"
 
@@ -40,7 +41,11 @@ struct Entry {
     float* v_scale;
     void* copy;
     double decay;  // 1 - lr weight_decay
+    int64_t vec;   // every array is aligned to eight of its elements (or 32 bytes)
 };
+
+template <int BITS> struct state_of { using type = float; };
+template <> struct state_of<8> { using type = uint8_t; };
 
 struct Scalars {
     float beta1, rest1, beta2, rest2;  // b, 1 - b
@@ -56,7 +61,7 @@ struct Scalars {
 template <int N>
 struct Table {
     Scalars s;
-    int32_t count;
+    int32_t count, blocks_per_warp;
     uint32_t first[N + 1];
     Entry e[N];
 };
@@ -92,23 +97,168 @@ template <typename P> __device__ __forceinline__ typename wide_of<P>::type widen
     else return to_f32(x);
 }
 
-template <typename P, typename G, int BITS, int N>
-__global__ void __launch_bounds__(kWarps * 32)
-adamw_kernel(const __grid_constant__ Table<N> tab) {
-    if (tab.s.status != nullptr && *tab.s.status != 0) return;
-    // the entry with first[i] <= blockIdx.x < first[i + 1]
-    int lo = 0, hi = tab.count - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (tab.first[mid] <= blockIdx.x) lo = mid; else hi = mid - 1;
+// Eight consecutive elements (8 to 64 bytes, aligned to that or to 32 bytes).
+template <typename T> struct Words {
+    static constexpr int kBytes = 8 * (int)sizeof(T);
+    uint32_t w[kBytes / 4];
+    __device__ __forceinline__ void load(const T* p) {
+        if constexpr (kBytes == 8) {
+            asm volatile("ld.global.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+        } else if constexpr (kBytes == 16) {
+            asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
+        } else {
+#pragma unroll
+            for (int i = 0; i < kBytes / 4; i += 8)
+                asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                             : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3]),
+                               "=r"(w[i + 4]), "=r"(w[i + 5]), "=r"(w[i + 6]), "=r"(w[i + 7])
+                             : "l"(reinterpret_cast<const uint32_t*>(p) + i));
+        }
     }
-    const Entry& e = tab.e[lo];
+    __device__ __forceinline__ void store(T* p) const {
+        if constexpr (kBytes == 8) {
+            asm volatile("st.global.v2.b32 [%2], {%0, %1};" ::"r"(w[0]), "r"(w[1]), "l"(p) : "memory");
+        } else if constexpr (kBytes == 16) {
+            asm volatile("st.global.v4.b32 [%4], {%0, %1, %2, %3};" ::
+                             "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "l"(p) : "memory");
+        } else {
+#pragma unroll
+            for (int i = 0; i < kBytes / 4; i += 8)
+                asm volatile("st.global.v8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::
+                                 "r"(w[i]), "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]),
+                                 "r"(w[i + 4]), "r"(w[i + 5]), "r"(w[i + 6]), "r"(w[i + 7]),
+                                 "l"(reinterpret_cast<uint32_t*>(p) + i) : "memory");
+        }
+    }
+    __device__ __forceinline__ double get_double(int i) const {
+        return __hiloint2double((int)w[2 * i + 1], (int)w[2 * i]);
+    }
+    __device__ __forceinline__ void set_double(int i, double x) {
+        w[2 * i] = (uint32_t)__double2loint(x), w[2 * i + 1] = (uint32_t)__double2hiint(x);
+    }
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (sizeof(T) == 8) f[i] = __double2float_rn(get_double(i));
+            else if constexpr (sizeof(T) == 4) f[i] = __uint_as_float(w[i]);
+            else if constexpr (sizeof(T) == 2) { if (i % 2 == 0) unpack2<T>(w[i / 2], f[i], f[i + 1]); }
+            else if (i % 2 == 0) {
+                const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((uint16_t)(w[i / 4] >> (8 * (i % 4))), __NV_E4M3);
+                const float2 q = __half22float2(__half2(h));
+                f[i] = q.x, f[i + 1] = q.y;
+            }
+        }
+    }
+    __device__ __forceinline__ void set(const float (&f)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(f[i]);
+            else if constexpr (sizeof(T) == 2) { if (i % 2 == 0) w[i / 2] = pack2<T>(f[i], f[i + 1]); }
+            else if (i % 4 == 0) {
+                w[i / 4] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(f[i], f[i + 1]), __NV_SATFINITE, __NV_E4M3) |
+                           (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(f[i + 2], f[i + 3]), __NV_SATFINITE,
+                                                              __NV_E4M3) << 16;
+            }
+        }
+    }
+};
+
+// Sums one by one: the packed sum may be contracted with a packed product.
+__device__ __forceinline__ void add8(float (&d)[8], const float (&a)[8], const float (&b)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) d[i] = __fadd_rn(a[i], b[i]);
+}
+
+// A whole block of a tensor whose arrays are aligned, eight consecutive
+// elements a lane; the same operations as the single elements below, products
+// two to an instruction.
+template <typename P, typename G, int BITS>
+__device__ __forceinline__ void whole_block(const Scalars& s, const Entry& e, int64_t block, int64_t at,
+                                            float gs) {
+    using S = typename state_of<BITS>::type;
     const int lane = threadIdx.x % 32;
-    const int64_t block = (int64_t)(blockIdx.x - tab.first[lo]) * kWarps + threadIdx.x / 32;
-    const int64_t at = block * kBlock;
-    if (at >= e.numel) return;
+    const int64_t j = at + lane * 8;
+    Words<P> wp;
+    Words<G> wg;
+    Words<S> wm, wv;
+    wg.load(static_cast<const G*>(e.grad) + j);
+    wm.load(static_cast<const S*>(e.m) + j);
+    wv.load(static_cast<const S*>(e.v) + j);
+    wp.load(static_cast<const P*>(e.param) + j);
+    float g[8], m[8], v[8], r[8], q[8];
+    wg.get(g);
+    scale_v<8>(g, g, gs);
+    wm.get(m);
+    if constexpr (BITS == 8) {
+        scale_v<8>(m, m, e.m_scale[block]);
+        wv.get(r);
+        scale_v<8>(r, r, e.v_scale[block]);
+        mul_v<8>(v, r, r);
+    } else {
+        wv.get(v);
+    }
+    scale_v<8>(m, m, s.beta1);
+    scale_v<8>(q, g, s.rest1);
+    add8(m, m, q);
+    scale_v<8>(v, v, s.beta2);
+    mul_v<8>(g, g, g);
+    scale_v<8>(g, g, s.rest2);
+    add8(v, v, g);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = __fsqrt_rn(v[i]);
+    float k[8];
+    fill_v<8>(k, s.eps);
+    scale_v<8>(q, r, s.root);
+    add8(q, q, k);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(m[i], q[i]);
+    scale_v<8>(q, q, -s.rate);  // what is added to the decayed parameter
+    if constexpr (sizeof(P) == 8) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            wp.set_double(i, __dadd_rn(__dmul_rn(wp.get_double(i), e.decay), (double)q[i]));
+        wp.store(static_cast<P*>(e.param) + j);
+    } else {
+        float p[8];
+        wp.get(p);
+        scale_v<8>(p, p, (float)e.decay);
+        add8(p, p, q);
+        wp.set(p);
+        wp.store(static_cast<P*>(e.param) + j);
+        if constexpr (sizeof(G) == 2 && sizeof(P) == 4) {
+            if (e.copy != nullptr) {
+                wg.set(p);
+                wg.store(static_cast<G*>(e.copy) + j);
+            }
+        }
+    }
+    if constexpr (BITS == 8) {
+        uint32_t mtop = 0, rtop = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mtop = max(mtop, abs_bits(m[i])), rtop = max(rtop, abs_bits(r[i]));
+        const float ms = block_scale(warp_max(mtop)), rs = block_scale(warp_max(rtop));
+        if (lane == 0) e.m_scale[block] = ms, e.v_scale[block] = rs;
+        scale_v<8>(m, m, __frcp_rn(ms));
+        wm.set(m);
+        scale_v<8>(q, r, __frcp_rn(rs));
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (r[i] > 0.0f && q[i] < 0x1p-9f) q[i] = 0x1p-9f;
+        wv.set(q);
+    } else {
+        wm.set(m);
+        wv.set(v);
+    }
+    wm.store(static_cast<S*>(e.m) + j);
+    wv.store(static_cast<S*>(e.v) + j);
+}
+
+// A block of any length and alignment, element by element.
+template <typename P, typename G, int BITS>
+__device__ __noinline__ void any_block(const Scalars& s, const Entry& e, int64_t block, int64_t at, float gs) {
+    const int lane = threadIdx.x % 32;
     const int n = (int)min((int64_t)kBlock, e.numel - at);
-    const float gs = tab.s.grad_scale != nullptr ? *tab.s.grad_scale : 1.0f;
     P* p = static_cast<P*>(e.param) + at;
     const G* g = static_cast<const G*>(e.grad) + at;
     G* copy = e.copy != nullptr ? static_cast<G*>(e.copy) + at : nullptr;
@@ -129,7 +279,7 @@ adamw_kernel(const __grid_constant__ Table<N> tab) {
             m[i] = static_cast<const float*>(e.m)[at + j];
             v[i] = static_cast<const float*>(e.v)[at + j];
         }
-        const float step = adam(tab.s, __fmul_rn(to_f32(g[j]), gs), m[i], v[i], r[i]);
+        const float step = adam(s, __fmul_rn(to_f32(g[j]), gs), m[i], v[i], r[i]);
         const auto w = decayed(widen<P>(p[j]), e.decay, step);
         p[j] = narrow<P>(w);
         if constexpr (sizeof(G) == 2 && sizeof(P) == 4)
@@ -158,28 +308,55 @@ adamw_kernel(const __grid_constant__ Table<N> tab) {
     }
 }
 
+template <typename P, typename G, int BITS, int N>
+__global__ void __launch_bounds__(kWarps * 32)
+adamw_kernel(const __grid_constant__ Table<N> tab) {
+    if (tab.s.status != nullptr && *tab.s.status != 0) return;
+    // the entry with first[i] <= blockIdx.x < first[i + 1]
+    int lo = 0, hi = tab.count - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (tab.first[mid] <= blockIdx.x) lo = mid; else hi = mid - 1;
+    }
+    const Entry& e = tab.e[lo];
+    const float gs = tab.s.grad_scale != nullptr ? *tab.s.grad_scale : 1.0f;
+    const int64_t first = (int64_t)(blockIdx.x - tab.first[lo]) * kWarps * tab.blocks_per_warp + threadIdx.x / 32;
+#pragma unroll 1
+    for (int i = 0; i < tab.blocks_per_warp; ++i) {
+        const int64_t block = first + i * kWarps, at = block * kBlock;
+        if (at >= e.numel) return;
+        if (e.vec && at + kBlock <= e.numel) whole_block<P, G, BITS>(tab.s, e, block, at, gs);
+        else any_block<P, G, BITS>(tab.s, e, block, at, gs);
+    }
+}
+
 template <int N, typename P, typename G, int BITS>
 cudaError_t launch(int64_t count, const chol_adamw_tensor* t, const AdamwArgs& a,
                    const Scalars& s, cudaStream_t stream) {
     std::unique_ptr<Table<N>> tab(new (std::nothrow) Table<N>);
     if (tab == nullptr) return cudaErrorMemoryAllocation;
     tab->s = s;
-    constexpr int64_t kChunk = (int64_t)kBlock * kWarps;
+    // a few blocks a warp, to look the entry up less often, once there are
+    // thread blocks enough for every SM
+    int64_t all = 0;
+    for (int64_t i = 0; i < count; ++i) all += (t[i].numel + kBlock - 1) / kBlock;
+    tab->blocks_per_warp = all >= (int64_t)device_sm_count() * kWarps * 64 ? 4 : 1;
+    const int64_t chunk = (int64_t)kBlock * kWarps * tab->blocks_per_warp;
     constexpr uint64_t kMaxGrid = 0x7fffffff;
     int64_t i = 0, done = 0;  // `done` thread blocks' worth of tensor i is launched already
     while (i < count) {
         uint64_t blocks = 0;
         tab->count = 0;
         while (i < count && tab->count < N && blocks < kMaxGrid) {
-            const int64_t from = done * kChunk;
+            const int64_t from = done * chunk;
             if (t[i].numel <= from) {
                 ++i, done = 0;
                 continue;
             }
-            const int64_t need = (t[i].numel - from + kChunk - 1) / kChunk;
+            const int64_t need = (t[i].numel - from + chunk - 1) / chunk;
             const int64_t take = (int64_t)std::min<uint64_t>(need, kMaxGrid - blocks);
             Entry& e = tab->e[tab->count];
-            e.numel = std::min<int64_t>(t[i].numel - from, take * kChunk);
+            e.numel = std::min<int64_t>(t[i].numel - from, take * chunk);
             e.param = static_cast<P*>(t[i].param) + from;
             e.grad = static_cast<const G*>(t[i].grad) + from;
             const int64_t state = from * (BITS / 8), block = from / kBlock;
@@ -189,6 +366,10 @@ cudaError_t launch(int64_t count, const chol_adamw_tensor* t, const AdamwArgs& a
             e.v_scale = BITS == 8 ? t[i].v_scale + block : nullptr;
             e.copy = t[i].copy != nullptr ? static_cast<G*>(t[i].copy) + from : nullptr;
             e.decay = 1.0 - a.lr * t[i].weight_decay;
+            const size_t ss = BITS == 8 ? 8 : 32;
+            e.vec = aligned(e.param, std::min<size_t>(8 * sizeof(P), 32)) &&
+                    aligned(e.grad, std::min<size_t>(8 * sizeof(G), 32)) && aligned(e.m, ss) &&
+                    aligned(e.v, ss) && (e.copy == nullptr || aligned(e.copy, 8 * sizeof(G)));
             tab->first[tab->count++] = (uint32_t)blocks;
             blocks += take;
             if (take == need) ++i, done = 0; else done += take;

@@ -59,8 +59,8 @@ __device__ __forceinline__ float rcp_fast(float x) {
     return y;
 }
 
-// d = a b + c, a b and a + b on V floats, two to an instruction (each rounded
-// as the scalar operation is).
+// d = a b + c, a b and a + b on V floats, two to an instruction.  A product and
+// a sum that uses it may be contracted to one rounding, .rn or not.
 template <int V>
 __device__ __forceinline__ void fma_v(float (&d)[V], const float (&a)[V], const float (&b)[V],
                                       const float (&c)[V]) {
