@@ -3,6 +3,14 @@
 //   g' = g s,  m = b1 m + (1 - b1) g',  v = b2 v + (1 - b2) g'^2
 //   p  = p (1 - lr wd) - lr / (1 - b1^t) * m / (sqrt(v) / sqrt(1 - b2^t) + eps)
 //
+// Bound by memory: a pass moves 28 bytes an element with float32 parameters,
+// bf16 gradients and a bf16 copy (1.06 ms for 268M elements, 7.1 TB/s), 10
+// bytes with bf16 parameters and 8-bit moments (0.71 ms for 400M, 5.7 TB/s;
+// there the 45 instructions an element share the bound).  A warp does one
+// block and ends: more blocks a warp measured slower (4: 0.91 ms), and so did
+// fetching the next block ahead (1.0 ms), since both take registers, and what
+// hides the loads is many warps (12 blocks of 4 warps on an SM, 40 registers).
+//
 // The tensors' addresses and sizes travel in the kernel's parameters, so a
 // call needs no device table and no copy.  A warp takes a block of 256
 // consecutive elements of one tensor, eight a lane: with 8-bit moments such a
@@ -11,9 +19,10 @@
 // m / scale and sqrt(v) / scale: sqrt(v) spans half of v's binades, so that
 // E4M3's seventeen reach v's from 1 down to 2^-34 of a block's largest.
 //
-// Each operation is rounded by itself (no contraction to fused multiply-adds),
-// so that the 8-bit codes are the same on every path and in any restatement
-// of the formulas in float32.
+// Each operation on the moments is rounded by itself (no contraction to fused
+// multiply-adds), so that the 8-bit codes are the same on every path and in
+// any restatement of the formulas in float32; the update of a parameter too,
+// but for approximate roots and quotients with 8-bit moments.
 
 #include <algorithm>
 #include <cmath>
@@ -28,7 +37,7 @@ namespace chol {
 namespace {
 
 constexpr int kBlock = 256;           // elements that share a scale
-constexpr int kWarps = 8;             // blocks of elements per thread block
+constexpr int kWarps = 4;              // blocks of elements per thread block
 constexpr int kPerLane = kBlock / 32;
 
 struct Entry {
@@ -40,8 +49,9 @@ struct Entry {
     float* m_scale;
     float* v_scale;
     void* copy;
-    double decay;  // 1 - lr weight_decay
-    int64_t vec;   // every array is aligned to eight of its elements (or 32 bytes)
+    double decay;    // 1 - lr weight_decay
+    float decay32;   // rounded
+    int32_t vec;     // every array is aligned to eight of its elements (or 32 bytes)
 };
 
 template <int BITS> struct state_of { using type = float; };
@@ -61,7 +71,7 @@ struct Scalars {
 template <int N>
 struct Table {
     Scalars s;
-    int32_t count, blocks_per_warp;
+    int32_t count;
     uint32_t first[N + 1];
     Entry e[N];
 };
@@ -80,11 +90,11 @@ __device__ __forceinline__ float adam(const Scalars& s, float g, float& m, float
     return __fmul_rn(__fdiv_rn(m, __fadd_rn(__fmul_rn(r, s.root), s.eps)), s.rate);
 }
 
-__device__ __forceinline__ float decayed(float p, double decay, float step) {
-    return __fsub_rn(__fmul_rn(p, (float)decay), step);
+__device__ __forceinline__ float decayed(float p, const Entry& e, float step) {
+    return __fsub_rn(__fmul_rn(p, e.decay32), step);
 }
-__device__ __forceinline__ double decayed(double p, double decay, float step) {
-    return __dsub_rn(__dmul_rn(p, decay), (double)step);
+__device__ __forceinline__ double decayed(double p, const Entry& e, float step) {
+    return __dsub_rn(__dmul_rn(p, e.decay), (double)step);
 }
 template <typename P> struct wide_of { using type = float; };
 template <> struct wide_of<double> { using type = double; };
@@ -170,88 +180,150 @@ __device__ __forceinline__ void add8(float (&d)[8], const float (&a)[8], const f
     for (int i = 0; i < 8; ++i) d[i] = __fadd_rn(a[i], b[i]);
 }
 
+// float64 from float32 and back (to nearest even) without the FP64 pipe, which
+// this chip has little of: the bits are moved, and what is no normal number is
+// left to the conversion instructions.
+__device__ __forceinline__ double to_f64(float x) {
+    const uint32_t b = __float_as_uint(x), m = b & 0x7fffffffu;
+    if (m - 0x00800000u >= 0x7f000000u) return (double)x;
+    return __hiloint2double((int)((b & 0x80000000u) | ((m >> 3) + (896u << 20))), (int)(m << 29));
+}
+__device__ __forceinline__ float from_f64(uint32_t lo, uint32_t hi) {
+    const uint32_t e = (hi >> 20) & 0x7ffu;
+    if (e - 897u >= 253u) return __double2float_rn(__hiloint2double((int)hi, (int)lo));
+    uint32_t t = __funnelshift_l(lo, hi, 3) - (384u << 23);  // exponent - 896, 23 bits of 52
+    t += ((lo & 0x1fffffffu) + (t & 1u)) > 0x10000000u;      // the rest: over half, or half and odd
+    return __uint_as_float((hi & 0x80000000u) | t);
+}
+
+// sqrt(x) within 2^-22, for any x >= 0.
+__device__ __forceinline__ float sqrt_near(float x) {
+    float y;
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// Whether one of the four bytes is 0.
+__device__ __forceinline__ bool zero_byte(uint32_t w) {
+    return ((w - 0x01010101u) & ~w & 0x80808080u) != 0;
+}
+
 // A whole block of a tensor whose arrays are aligned, eight consecutive
 // elements a lane; the same operations as the single elements below, products
 // two to an instruction.
 template <typename P, typename G, int BITS>
-__device__ __forceinline__ void whole_block(const Scalars& s, const Entry& e, int64_t block, int64_t at,
-                                            float gs) {
+__device__ __forceinline__ void whole_block(const Scalars& s, const Entry& e, int64_t block, float gs) {
     using S = typename state_of<BITS>::type;
-    const int lane = threadIdx.x % 32;
-    const int64_t j = at + lane * 8;
-    Words<P> wp;
-    Words<G> wg;
-    Words<S> wm, wv;
-    wg.load(static_cast<const G*>(e.grad) + j);
-    wm.load(static_cast<const S*>(e.m) + j);
-    wv.load(static_cast<const S*>(e.v) + j);
-    wp.load(static_cast<const P*>(e.param) + j);
-    float g[8], m[8], v[8], r[8], q[8];
-    wg.get(g);
-    scale_v<8>(g, g, gs);
-    wm.get(m);
-    if constexpr (BITS == 8) {
-        scale_v<8>(m, m, e.m_scale[block]);
-        wv.get(r);
-        scale_v<8>(r, r, e.v_scale[block]);
-        mul_v<8>(v, r, r);
-    } else {
-        wv.get(v);
-    }
-    scale_v<8>(m, m, s.beta1);
-    scale_v<8>(q, g, s.rest1);
-    add8(m, m, q);
-    scale_v<8>(v, v, s.beta2);
-    mul_v<8>(g, g, g);
-    scale_v<8>(g, g, s.rest2);
-    add8(v, v, g);
+    const int64_t j = block * kBlock + threadIdx.x % 32 * 8;
+    Words<P> p;
+    Words<G> g;
+    Words<S> m, v;
+    float m_scale = 0.0f, v_scale = 0.0f;
+    g.load(static_cast<const G*>(e.grad) + j);
+    m.load(static_cast<const S*>(e.m) + j);
+    v.load(static_cast<const S*>(e.v) + j);
+    p.load(static_cast<const P*>(e.param) + j);
+    if constexpr (BITS == 8) m_scale = e.m_scale[block], v_scale = e.v_scale[block];
+    float fg[8], fm[8], fv[8], r[8], q[8], k[8];
+    if constexpr (sizeof(G) == 8) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = __fsqrt_rn(v[i]);
-    float k[8];
+        for (int i = 0; i < 8; ++i) fg[i] = from_f64(g.w[2 * i], g.w[2 * i + 1]);
+    } else {
+        g.get(fg);
+    }
+    scale_v<8>(fg, fg, gs);
+    m.get(fm);
+    if constexpr (BITS == 8) {
+        scale_v<8>(fm, fm, m_scale);
+        v.get(r);
+        scale_v<8>(r, r, v_scale);
+        mul_v<8>(fv, r, r);
+    } else {
+        v.get(fv);
+    }
+    scale_v<8>(fm, fm, s.beta1);
+    scale_v<8>(q, fg, s.rest1);
+    add8(fm, fm, q);
+    scale_v<8>(fv, fv, s.beta2);
+    mul_v<8>(fg, fg, fg);
+    scale_v<8>(fg, fg, s.rest2);
+    add8(fv, fv, fg);
+    // 8-bit moments: approximate roots and quotients serve the parameter
+    // (two units of float32 in the update), and the codes where they
+    // cannot be off (below)
+    constexpr bool kExact = BITS == 32 || sizeof(P) == 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = kExact ? __fsqrt_rn(fv[i]) : sqrt_near(fv[i]);
     fill_v<8>(k, s.eps);
     scale_v<8>(q, r, s.root);
     add8(q, q, k);
+    if constexpr (kExact) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(m[i], q[i]);
+        for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(fm[i], q[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = __fdividef(fm[i], q[i]);
+    }
     scale_v<8>(q, q, -s.rate);  // what is added to the decayed parameter
     if constexpr (sizeof(P) == 8) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            wp.set_double(i, __dadd_rn(__dmul_rn(wp.get_double(i), e.decay), (double)q[i]));
-        wp.store(static_cast<P*>(e.param) + j);
+            p.set_double(i, __dadd_rn(__dmul_rn(p.get_double(i), e.decay), to_f64(q[i])));
     } else {
-        float p[8];
-        wp.get(p);
-        scale_v<8>(p, p, (float)e.decay);
-        add8(p, p, q);
-        wp.set(p);
-        wp.store(static_cast<P*>(e.param) + j);
+        float f[8];
+        p.get(f);
+        scale_v<8>(f, f, e.decay32);
+        add8(f, f, q);
+        p.set(f);
         if constexpr (sizeof(G) == 2 && sizeof(P) == 4) {
             if (e.copy != nullptr) {
-                wg.set(p);
-                wg.store(static_cast<G*>(e.copy) + j);
+                g.set(f);
+                g.store(static_cast<G*>(e.copy) + j);
             }
         }
     }
+    p.store(static_cast<P*>(e.param) + j);
     if constexpr (BITS == 8) {
-        uint32_t mtop = 0, rtop = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) mtop = max(mtop, abs_bits(m[i])), rtop = max(rtop, abs_bits(r[i]));
-        const float ms = block_scale(warp_max(mtop)), rs = block_scale(warp_max(rtop));
-        if (lane == 0) e.m_scale[block] = ms, e.v_scale[block] = rs;
-        scale_v<8>(m, m, __frcp_rn(ms));
-        wm.set(m);
-        scale_v<8>(q, r, __frcp_rn(rs));
+        // the largest root is the root of the largest v
+        uint32_t mtop = 0, vtop = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (r[i] > 0.0f && q[i] < 0x1p-9f) q[i] = 0x1p-9f;
-        wv.set(q);
+            mtop = max(mtop, abs_bits(fm[i])), vtop = max(vtop, __float_as_uint(fv[i]));
+        const float ms = block_scale(warp_max(mtop));
+        const float rs = block_scale(__float_as_uint(__fsqrt_rn(__uint_as_float(warp_max(vtop)))));
+        if (threadIdx.x % 32 == 0) e.m_scale[block] = ms, e.v_scale[block] = rs;
+        scale_v<8>(fm, fm, __frcp_rn(ms));
+        m.set(fm);
+        const float inv = __frcp_rn(rs);
+        bool sure = true;
+        if constexpr (!kExact) {
+            // the root is within 2^-22 of r: the code is that of the rounded
+            // root unless it changes between r (1 - 2^-20) and r (1 + 2^-20)
+            Words<S> above;
+            scale_v<8>(q, r, inv);
+            scale_v<8>(k, q, 1.0f + 0x1p-20f);
+            scale_v<8>(q, q, 1.0f - 0x1p-20f);
+            v.set(q);
+            above.set(k);
+            sure = v.w[0] == above.w[0] && v.w[1] == above.w[1];
+            // a code of 0 may be of a root above 0
+            sure = sure && !zero_byte(v.w[0]) && !zero_byte(v.w[1]);
+        } else {
+            sure = false;
+        }
+        if (!sure) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                q[i] = __fmul_rn(__fsqrt_rn(fv[i]), inv);
+                if (fv[i] > 0.0f && q[i] < 0x1p-9f) q[i] = 0x1p-9f;
+            }
+            v.set(q);
+        }
     } else {
-        wm.set(m);
-        wv.set(v);
+        m.set(fm);
+        v.set(fv);
     }
-    wm.store(static_cast<S*>(e.m) + j);
-    wv.store(static_cast<S*>(e.v) + j);
+    m.store(static_cast<S*>(e.m) + j);
+    v.store(static_cast<S*>(e.v) + j);
 }
 
 // A block of any length and alignment, element by element.
@@ -280,7 +352,7 @@ __device__ __noinline__ void any_block(const Scalars& s, const Entry& e, int64_t
             v[i] = static_cast<const float*>(e.v)[at + j];
         }
         const float step = adam(s, __fmul_rn(to_f32(g[j]), gs), m[i], v[i], r[i]);
-        const auto w = decayed(widen<P>(p[j]), e.decay, step);
+        const auto w = decayed(widen<P>(p[j]), e, step);
         p[j] = narrow<P>(w);
         if constexpr (sizeof(G) == 2 && sizeof(P) == 4)
             if (copy != nullptr) copy[j] = from_f32<G>(w);
@@ -309,7 +381,7 @@ __device__ __noinline__ void any_block(const Scalars& s, const Entry& e, int64_t
 }
 
 template <typename P, typename G, int BITS, int N>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, BITS == 8 && sizeof(P) < 8 ? 12 : 1)
 adamw_kernel(const __grid_constant__ Table<N> tab) {
     if (tab.s.status != nullptr && *tab.s.status != 0) return;
     // the entry with first[i] <= blockIdx.x < first[i + 1]
@@ -320,14 +392,11 @@ adamw_kernel(const __grid_constant__ Table<N> tab) {
     }
     const Entry& e = tab.e[lo];
     const float gs = tab.s.grad_scale != nullptr ? *tab.s.grad_scale : 1.0f;
-    const int64_t first = (int64_t)(blockIdx.x - tab.first[lo]) * kWarps * tab.blocks_per_warp + threadIdx.x / 32;
-#pragma unroll 1
-    for (int i = 0; i < tab.blocks_per_warp; ++i) {
-        const int64_t block = first + i * kWarps, at = block * kBlock;
-        if (at >= e.numel) return;
-        if (e.vec && at + kBlock <= e.numel) whole_block<P, G, BITS>(tab.s, e, block, at, gs);
-        else any_block<P, G, BITS>(tab.s, e, block, at, gs);
-    }
+    const int64_t block = (int64_t)(blockIdx.x - tab.first[lo]) * kWarps + threadIdx.x / 32;
+    const int64_t at = block * kBlock;
+    if (at >= e.numel) return;
+    if (e.vec && at + kBlock <= e.numel) whole_block<P, G, BITS>(tab.s, e, block, gs);
+    else any_block<P, G, BITS>(tab.s, e, block, at, gs);
 }
 
 template <int N, typename P, typename G, int BITS>
@@ -336,12 +405,7 @@ cudaError_t launch(int64_t count, const chol_adamw_tensor* t, const AdamwArgs& a
     std::unique_ptr<Table<N>> tab(new (std::nothrow) Table<N>);
     if (tab == nullptr) return cudaErrorMemoryAllocation;
     tab->s = s;
-    // a few blocks a warp, to look the entry up less often, once there are
-    // thread blocks enough for every SM
-    int64_t all = 0;
-    for (int64_t i = 0; i < count; ++i) all += (t[i].numel + kBlock - 1) / kBlock;
-    tab->blocks_per_warp = all >= (int64_t)device_sm_count() * kWarps * 64 ? 4 : 1;
-    const int64_t chunk = (int64_t)kBlock * kWarps * tab->blocks_per_warp;
+    constexpr int64_t chunk = (int64_t)kBlock * kWarps;
     constexpr uint64_t kMaxGrid = 0x7fffffff;
     int64_t i = 0, done = 0;  // `done` thread blocks' worth of tensor i is launched already
     while (i < count) {
@@ -366,6 +430,7 @@ cudaError_t launch(int64_t count, const chol_adamw_tensor* t, const AdamwArgs& a
             e.v_scale = BITS == 8 ? t[i].v_scale + block : nullptr;
             e.copy = t[i].copy != nullptr ? static_cast<G*>(t[i].copy) + from : nullptr;
             e.decay = 1.0 - a.lr * t[i].weight_decay;
+            e.decay32 = (float)e.decay;
             const size_t ss = BITS == 8 ? 8 : 32;
             e.vec = aligned(e.param, std::min<size_t>(8 * sizeof(P), 32)) &&
                     aligned(e.grad, std::min<size_t>(8 * sizeof(G), 32)) && aligned(e.m, ss) &&
@@ -388,7 +453,7 @@ cudaError_t launch(int64_t count, const chol_adamw_tensor* t, const AdamwArgs& a
 template <typename P, typename G, int BITS>
 cudaError_t by_count(int64_t count, const chol_adamw_tensor* t, const AdamwArgs& a,
                      const Scalars& s, cudaStream_t stream) {
-    return count <= 48 ? launch<48, P, G, BITS>(count, t, a, s, stream)
+    return count <= 44 ? launch<44, P, G, BITS>(count, t, a, s, stream)
                        : launch<360, P, G, BITS>(count, t, a, s, stream);
 }
 

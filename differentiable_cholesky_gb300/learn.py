@@ -71,14 +71,24 @@ def _ptr(x):
     return None if x is None else x.data_ptr()
 
 
-def _on(stream, inputs, call):
-    """``call()`` with ``stream`` as the current one: what it allocates belongs
-    to that stream, and the inputs' memory is not given to others before its
-    work is done."""
+def _like(x: torch.Tensor) -> torch.Tensor:
+    """An uninitialised contiguous tensor like ``x``."""
+    return torch.empty_like(x, memory_format=torch.contiguous_format)
+
+
+def _current(x: torch.Tensor) -> int:
+    """The current stream of a tensor's device."""
+    return torch._C._cuda_getCurrentRawStream(x.get_device())
+
+
+def _on(stream, inputs, call, *args):
+    """``call(*args)`` with ``stream`` as the current one: what it allocates
+    belongs to that stream, and the inputs' memory is not given to others
+    before its work is done."""
     if stream is None:
-        return call()
+        return call(*args)
     with torch.cuda.stream(stream):
-        out = call()
+        out = call(*args)
     for x in inputs:
         if x is not None:
             x.record_stream(stream)
@@ -102,7 +112,7 @@ def _f32(x, name: str, shape, like: torch.Tensor):
         return
     if not isinstance(x, torch.Tensor) or x.device != like.device:
         raise ValueError(f"{name} must be a tensor on {like.device}")
-    if x.dtype != torch.float32 or tuple(x.shape) != tuple(shape) or not x.is_contiguous():
+    if x.dtype != torch.float32 or x.shape != shape or not x.is_contiguous():
         raise ValueError(f"{name} must be contiguous float32 {tuple(shape)}, "
                          f"got {x.dtype} {tuple(x.shape)}")
 
@@ -130,54 +140,54 @@ def _rows(x: torch.Tensor, name: str):
     return rows, d, ld
 
 
-def _same_shape(x, y, names):
-    if tuple(x.shape) != tuple(y.shape):
-        raise ValueError(f"{names[0]} must match {names[1]}'s shape {tuple(y.shape)}, "
-                         f"got {tuple(x.shape)}")
-
-
 # ----------------------------------------------------------------------------
 # Root-mean-square norm
 # ----------------------------------------------------------------------------
+def _weight(weight, x, d):
+    if weight is not None:
+        _model(weight, "weight", x)
+        if weight.dim() != 1 or weight.numel() != d or not weight.is_contiguous():
+            raise ValueError(f"weight must be contiguous [{d}], got {tuple(weight.shape)}")
+
+
 def _rms_forward(x, weight, residual, eps, code, group, stream):
     _model(x, "x")
     rows, d, ldx = _rows(x, "x")
     if d == 0:
         raise ValueError("x must have at least one column")
-    if weight is not None:
-        _model(weight, "weight", x)
-        if tuple(weight.shape) != (d,) or not weight.is_contiguous():
-            raise ValueError(f"weight must be contiguous [{d}], got {tuple(weight.shape)}")
+    _weight(weight, x, d)
     ldr, rtype = d, x.dtype
     if residual is not None:
         _model(residual, "residual")
-        _same_shape(residual, x, ("residual", "x"))
-        if residual.device != x.device:
-            raise ValueError(f"residual must be on {x.device}")
+        if residual.shape != x.shape or residual.device != x.device:
+            raise ValueError(f"residual must be {tuple(x.shape)} on {x.device}, "
+                             f"got {tuple(residual.shape)} on {residual.device}")
         rtype = residual.dtype
         if rtype != x.dtype and rtype != torch.float32:
             raise ValueError(f"residual must have dtype {x.dtype} or float32, got {rtype}")
         ldr = _rows(residual, "residual")[2]
+    return _on(stream, (x, weight, residual), _rms_run, x, weight, residual, eps, code, group,
+               rows, d, ldx, ldr, rtype)
 
-    def call():
-        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-        r = torch.empty(x.shape, dtype=rtype, device=x.device) if residual is not None else None
-        scale = None
-        if code is None:
-            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-            ytype = _MODEL[x.dtype]
-        else:
-            ytype = code[0]
-            y = torch.empty(x.shape, dtype=code[1], device=x.device)
-            groups = -(-d // group) if group else 1
-            scale = torch.empty(x.shape[:-1] + (groups,), dtype=torch.float32, device=x.device)
-        _check(_library().chol_rms_norm(
-            rows, d, _MODEL[x.dtype], _MODEL[rtype], ytype, group, eps, x.data_ptr(), ldx,
-            _ptr(residual), ldr, _ptr(weight), y.data_ptr(), _ptr(scale), _ptr(r),
-            rstd.data_ptr(), _b._stream_ptr(stream)))
-        return y, scale, x if r is None else r, rstd
 
-    return _on(stream, (x, weight, residual), call)
+def _rms_run(x, weight, residual, eps, code, group, rows, d, ldx, ldr, rtype):
+    lead, dev = x.shape[:-1], x.device
+    rstd = torch.empty(lead, dtype=torch.float32, device=dev)
+    r = None if residual is None else _like(residual)
+    scale = None
+    kind = ytype = _MODEL[x.dtype]
+    if code is None:
+        y = _like(x)
+    else:
+        ytype = code[0]
+        y = torch.empty(x.shape, dtype=code[1], device=dev)
+        scale = torch.empty(lead + (-(-d // group) if group else 1,), dtype=torch.float32, device=dev)
+    rc = _library().chol_rms_norm(
+        rows, d, kind, _MODEL[rtype], ytype, group, eps, x.data_ptr(), ldx, _ptr(residual), ldr,
+        _ptr(weight), y.data_ptr(), _ptr(scale), _ptr(r), rstd.data_ptr(), _current(x))
+    if rc:
+        _check(rc)
+    return y, scale, x if r is None else r, rstd
 
 
 def rms_norm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None,
@@ -216,7 +226,8 @@ def rms_norm_adj(adj_y: torch.Tensor, r: torch.Tensor, rstd: torch.Tensor,
     ``x`` alike; ``adj_weight`` is None without a weight or ``want_weight``."""
     _model(adj_y, "adj_y")
     _model(r, "r")
-    _same_shape(r, adj_y, ("r", "adj_y"))
+    if r.shape != adj_y.shape:
+        raise ValueError(f"r must match adj_y's shape {tuple(adj_y.shape)}, got {tuple(r.shape)}")
     if r.device != adj_y.device or (r.dtype != adj_y.dtype and r.dtype != torch.float32):
         raise ValueError(f"r must have dtype {adj_y.dtype} or float32 on {adj_y.device}, "
                          f"got {r.dtype} on {r.device}")
@@ -224,36 +235,35 @@ def rms_norm_adj(adj_y: torch.Tensor, r: torch.Tensor, rstd: torch.Tensor,
     if d == 0:
         raise ValueError("adj_y must have at least one column")
     ldr = _rows(r, "r")[2]
-    _f32(rstd, "rstd", adj_y.shape[:-1], adj_y)
     if rstd is None:
         raise ValueError("rstd is needed")
-    if weight is not None:
-        _model(weight, "weight", adj_y)
-        if tuple(weight.shape) != (d,) or not weight.is_contiguous():
-            raise ValueError(f"weight must be contiguous [{d}], got {tuple(weight.shape)}")
+    _f32(rstd, "rstd", adj_y.shape[:-1], adj_y)
+    _weight(weight, adj_y, d)
     if adj_r is not None:
         _model(adj_r, "adj_r", r)
-        _same_shape(adj_r, adj_y, ("adj_r", "adj_y"))
-        if not adj_r.is_contiguous():
-            raise ValueError("adj_r must be contiguous")
-    want_weight = want_weight and weight is not None
+        if adj_r.shape != adj_y.shape or not adj_r.is_contiguous():
+            raise ValueError(f"adj_r must be contiguous {tuple(adj_y.shape)}, "
+                             f"got {tuple(adj_r.shape)}")
+    return _on(stream, (adj_y, r, rstd, weight, adj_r), _rms_adj_run, adj_y, r, rstd, weight, adj_r,
+               want_weight and weight is not None, rows, d, ldy, ldr)
 
-    def call():
-        lib = _library()
-        adj_in = torch.empty(r.shape, dtype=r.dtype, device=r.device)
-        adj_w = work = None
-        need = 0
-        if want_weight:
-            adj_w = torch.empty_like(weight)
-            need = lib.chol_rms_norm_adj_workspace(rows, d)
-            work = torch.empty(need, dtype=torch.uint8, device=r.device)
-        _check(lib.chol_rms_norm_adj(
-            rows, d, _MODEL[adj_y.dtype], _MODEL[r.dtype], adj_y.data_ptr(), ldy, r.data_ptr(),
-            ldr, _ptr(weight), rstd.data_ptr(), _ptr(adj_r), adj_in.data_ptr(), None, _ptr(adj_w),
-            _ptr(work) if need else None, need, _b._stream_ptr(stream)))
-        return adj_in, adj_w
 
-    return _on(stream, (adj_y, r, rstd, weight, adj_r), call)
+def _rms_adj_run(adj_y, r, rstd, weight, adj_r, want_weight, rows, d, ldy, ldr):
+    lib = _library()
+    adj_in = _like(r)
+    adj_w = work = None
+    need = 0
+    if want_weight:
+        adj_w = torch.empty_like(weight)
+        need = lib.chol_rms_norm_adj_workspace(rows, d)
+        work = torch.empty(need, dtype=torch.uint8, device=r.device) if need else None
+    rc = lib.chol_rms_norm_adj(
+        rows, d, _MODEL[adj_y.dtype], _MODEL[r.dtype], adj_y.data_ptr(), ldy, r.data_ptr(), ldr,
+        _ptr(weight), rstd.data_ptr(), _ptr(adj_r), adj_in.data_ptr(), None, _ptr(adj_w),
+        _ptr(work), need, _current(r))
+    if rc:
+        _check(rc)
+    return adj_in, adj_w
 
 
 class _RmsNorm(torch.autograd.Function):
@@ -293,8 +303,8 @@ def _sequence(x, name: str, packed: bool, like=None):
     if x.dim() not in ((2,) if packed else (2, 3)):
         raise ValueError(f"{name} must be [T, D]{'' if packed else ' or [B, T, D]'}, "
                          f"got {tuple(x.shape)}")
-    if like is not None:
-        _same_shape(x, like, (name, "x"))
+    if like is not None and x.shape != like.shape:
+        raise ValueError(f"{name} must match x's shape {tuple(like.shape)}, got {tuple(x.shape)}")
     batch, (time, d) = (x.shape[0] if x.dim() == 3 else 1), x.shape[-2:]
     ts, bs = x.stride(-2), (x.stride(0) if x.dim() == 3 else 0)
     if d == 0:
@@ -333,20 +343,21 @@ def linrec_fwd(gate: torch.Tensor, x: torch.Tensor, state: torch.Tensor | None =
     ``S`` sequences one behind another, of any lengths, also none.  ``state``
     (float32 ``[B or S, D]``) is what each begins with, zeros by default; the
     returned one is what each ends with, not rounded to ``x``'s type."""
-    shape, (gbs, gts), n = _recurrence(gate, x, state, offsets, kind)
+    shape, strides, n = _recurrence(gate, x, state, offsets, kind)
+    return _on(stream, (gate, x, state, offsets), _linrec_run, gate, x, state, offsets, _GATES[kind],
+               bool(complement), shape, strides, n)
+
+
+def _linrec_run(gate, x, state, offsets, kind, complement, shape, strides, n):
     batch, time, d, bs, ts = shape
-
-    def call():
-        lib = _library()
-        h = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        last = torch.empty((n, d), dtype=torch.float32, device=x.device)
-        _check(lib.chol_linrec(
-            batch, time, d, _MODEL[x.dtype], _GATES[kind], int(complement), gate.data_ptr(), gbs,
-            gts, x.data_ptr(), bs, ts, _ptr(state), _ptr(offsets), n, h.data_ptr(),
-            last.data_ptr(), _b._stream_ptr(stream)))
-        return h, last
-
-    return _on(stream, (gate, x, state, offsets), call)
+    h = _like(x)
+    last = torch.empty((n, d), dtype=torch.float32, device=x.device)
+    rc = _library().chol_linrec(
+        batch, time, d, _MODEL[x.dtype], kind, complement, gate.data_ptr(), *strides, x.data_ptr(),
+        bs, ts, _ptr(state), _ptr(offsets), n, h.data_ptr(), last.data_ptr(), _current(x))
+    if rc:
+        _check(rc)
+    return h, last
 
 
 def linrec_step(gate: torch.Tensor, x: torch.Tensor, state: torch.Tensor, kind: str = "logit",
@@ -357,26 +368,29 @@ def linrec_step(gate: torch.Tensor, x: torch.Tensor, state: torch.Tensor, kind: 
         raise ValueError(f"unknown kind {kind!r}; expected one of {sorted(_GATES)}")
     _model(x, "x")
     _model(gate, "gate", x)
-    _same_shape(gate, x, ("gate", "x"))
-    if x.dim() != 2 or x.shape[1] == 0:
-        raise ValueError(f"x must be [B, D], got {tuple(x.shape)}")
+    if x.dim() != 2 or x.shape[1] == 0 or gate.shape != x.shape:
+        raise ValueError(f"x and gate must be [B, D], got {tuple(x.shape)} and {tuple(gate.shape)}")
     batch, d = x.shape
-    for name, t in (("x", x), ("gate", gate)):
-        if (t.stride(1) != 1 and d > 1) or (t.stride(0) < d and batch > 1):
-            raise ValueError(f"{name} must have contiguous channels, got strides {t.stride()}")
+    (xs, x1), (gs, g1) = x.stride(), gate.stride()
+    if (d > 1 and (x1 != 1 or g1 != 1)) or (batch > 1 and (xs < d or gs < d)):
+        raise ValueError(f"x and gate must have contiguous channels, got strides {x.stride()} and "
+                         f"{gate.stride()}")
     if state is None:
         raise ValueError("state is needed")
-    _f32(state, "state", (batch, d), x)
+    _f32(state, "state", x.shape, x)
+    return _on(stream, (gate, x, state), _step_run, gate, x, state, _GATES[kind], bool(complement),
+               batch, d, gs, xs)
 
-    def call():
-        h = torch.empty((batch, d), dtype=x.dtype, device=x.device)
-        _check(_library().chol_linrec(
-            batch, 1, d, _MODEL[x.dtype], _GATES[kind], int(complement), gate.data_ptr(),
-            gate.stride(0), d, x.data_ptr(), x.stride(0), d, state.data_ptr(), None, batch,
-            h.data_ptr(), state.data_ptr(), _b._stream_ptr(stream)))
-        return h
 
-    return _on(stream, (gate, x, state), call)
+def _step_run(gate, x, state, kind, complement, batch, d, gs, xs):
+    h = _like(x)
+    at = state.data_ptr()
+    rc = _library().chol_linrec(batch, 1, d, _MODEL[x.dtype], kind, complement, gate.data_ptr(), gs,
+                                d, x.data_ptr(), xs, d, at, None, batch, h.data_ptr(), at,
+                                _current(x))
+    if rc:
+        _check(rc)
+    return h
 
 
 def linrec_adj(gate: torch.Tensor, x: torch.Tensor, h: torch.Tensor, adj_h: torch.Tensor,
@@ -387,28 +401,30 @@ def linrec_adj(gate: torch.Tensor, x: torch.Tensor, h: torch.Tensor, adj_h: torc
     gradients ``adj_h`` of ``h`` and ``adj_state`` of the final states (zeros by
     default).  ``h`` is the forward's output; ``adj_state0`` is the gradient of
     the initial states."""
-    shape, (gbs, gts), n = _recurrence(gate, x, state, offsets, kind)
-    batch, time, d, bs, ts = shape
-    dbs, dts = _sequence(adj_h, "adj_h", offsets is not None, x)[3:]
+    shape, strides, n = _recurrence(gate, x, state, offsets, kind)
+    adj_strides = _sequence(adj_h, "adj_h", offsets is not None, x)[3:]
     _model(h, "h", x)
-    _same_shape(h, x, ("h", "x"))
-    if not h.is_contiguous():
-        raise ValueError("h must be contiguous")
-    _f32(adj_state, "adj_state", (n, d), x)
+    if h.shape != x.shape or not h.is_contiguous():
+        raise ValueError(f"h must be contiguous {tuple(x.shape)}, got {tuple(h.shape)}")
+    _f32(adj_state, "adj_state", (n, shape[2]), x)
+    return _on(stream, (gate, x, h, adj_h, state, adj_state, offsets), _linrec_adj_run, gate, x, h,
+               adj_h, state, adj_state, offsets, _GATES[kind], bool(complement), shape, strides,
+               adj_strides, n)
 
-    def call():
-        lib = _library()
-        adj_g = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        adj_x = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        adj_0 = torch.empty((n, d), dtype=torch.float32, device=x.device)
-        _check(lib.chol_linrec_adj(
-            batch, time, d, _MODEL[x.dtype], _GATES[kind], int(complement), gate.data_ptr(), gbs,
-            gts, x.data_ptr(), bs, ts, _ptr(state), _ptr(offsets), n, h.data_ptr(),
-            adj_h.data_ptr(), dbs, dts, _ptr(adj_state), adj_g.data_ptr(), adj_x.data_ptr(),
-            adj_0.data_ptr(), _b._stream_ptr(stream)))
-        return adj_g, adj_x, adj_0
 
-    return _on(stream, (gate, x, h, adj_h, state, adj_state, offsets), call)
+def _linrec_adj_run(gate, x, h, adj_h, state, adj_state, offsets, kind, complement, shape, strides,
+                    adj_strides, n):
+    batch, time, d, bs, ts = shape
+    adj_g = _like(x)
+    adj_x = _like(x)
+    adj_0 = torch.empty((n, d), dtype=torch.float32, device=x.device)
+    rc = _library().chol_linrec_adj(
+        batch, time, d, _MODEL[x.dtype], kind, complement, gate.data_ptr(), *strides, x.data_ptr(),
+        bs, ts, _ptr(state), _ptr(offsets), n, h.data_ptr(), adj_h.data_ptr(), *adj_strides,
+        _ptr(adj_state), adj_g.data_ptr(), adj_x.data_ptr(), adj_0.data_ptr(), _current(x))
+    if rc:
+        _check(rc)
+    return adj_g, adj_x, adj_0
 
 
 class _Linrec(torch.autograd.Function):
@@ -463,7 +479,7 @@ class AdamW:
     tensors are updated in place.
 
     :attr:`m`, :attr:`v` (and :attr:`m_scale`, :attr:`v_scale`) are the
-    moments, one tensor for each parameter."""
+    moments, one tensor for each parameter, in memory that stays the same."""
 
     def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
                  weight_decay=1e-2, state_bits: int = 32, copies=None, state=None):
@@ -477,9 +493,10 @@ class AdamW:
             raise ValueError("weight_decay must be a number, or one for each parameter")
         self.lr, self.betas, self.eps, self.state_bits = float(lr), tuple(betas), float(eps), state_bits
         self.steps = 0
-        self.copies = [None] * n if copies is None else list(copies)
+        self.copies = (None,) * n if copies is None else tuple(copies)
         if len(self.copies) != n:
             raise ValueError("copies must have an entry for each parameter")
+        self._copied = any(c is not None for c in self.copies)
         for i, p in enumerate(self.params):
             if not isinstance(p, torch.Tensor) or not p.is_cuda or p.dtype not in _PARAM:
                 raise ValueError(f"parameter {i} must be a CUDA tensor of a floating type of 16 "
@@ -497,6 +514,11 @@ class AdamW:
         t = self._table
         t["numel"] = [p.numel() for p in self.params]
         t["weight_decay"] = decay
+        # the optimiser's own tensors stay where they are
+        for name in ("m", "v", "m_scale", "v_scale"):
+            if getattr(self, name) is not None:
+                t[name] = [x.data_ptr() for x in getattr(self, name)]
+        t["copy"] = [0 if c is None else c.data_ptr() for c in self.copies]
 
     def _new_state(self):
         """Zero moments: one allocation for each kind, tensors from 256 to 256."""
@@ -539,7 +561,7 @@ class AdamW:
                         or not x.is_contiguous():
                     raise ValueError(f"state {name}[{i}] must be contiguous {want} with {count} "
                                      "elements")
-            got[name] = xs
+            got[name] = tuple(xs)
         step = int(state["step"])
         if step < 0:
             raise ValueError("state step must not be negative")
@@ -577,51 +599,62 @@ class AdamW:
         every gradient (a clipping factor, or one over the loss's scale);
         ``status`` an int32 one: where it is not 0 on the device nothing is
         written (the step is still counted)."""
-        grads = [p.grad for p in self.params] if grads is None else list(grads)
-        if len(grads) != len(self.params):
+        params = self.params
+        grads = [p.grad for p in params] if grads is None else list(grads)
+        if len(grads) != len(params):
             raise ValueError("grads must have an entry for each parameter")
-        dev = self.params[0].device if self.params else None
+        if not params:
+            self.steps += 1
+            return
+        dev = params[0].device
         for name, x, kind in (("grad_scale", grad_scale, torch.float32),
                               ("status", status, torch.int32)):
             if x is not None and (x.dtype != kind or x.numel() != 1 or x.device != dev):
                 raise ValueError(f"{name} must be one {kind} value on {dev}")
         calls = {}
-        for i, (p, g) in enumerate(zip(self.params, grads)):
+        index = params[0].get_device()
+        for i, g in enumerate(grads):
             if g is None:
                 continue
-            if g.dtype not in _GRADS[p.dtype] or g.device != dev or g.numel() != p.numel() \
+            p = params[i]
+            pt, gt = p.dtype, g.dtype
+            if gt not in _GRADS[pt] or g.get_device() != index or g.numel() != p.numel() \
                     or not g.is_contiguous():
                 raise ValueError(f"gradient {i} must be contiguous with its parameter's shape, of "
-                                 f"a type in {_GRADS[p.dtype]}, got {g.dtype} {tuple(g.shape)}")
-            c = self.copies[i]
-            if c is not None and c.dtype != g.dtype:
-                raise ValueError(f"copy {i} must have its gradient's dtype {g.dtype}")
-            calls.setdefault((p.dtype, g.dtype), []).append(i)
-        lr = self.lr if lr is None else float(lr)
-
-        def call():
-            for (pt, gt), at in calls.items():
-                whole = len(at) == len(self.params)
-                t = self._table.copy() if whole else self._table[at]
-                pick = (lambda xs: xs) if whole else (lambda xs: [xs[i] for i in at])
-                t["param"] = [x.data_ptr() for x in pick(self.params)]
-                t["grad"] = [x.data_ptr() for x in pick(grads)]
-                t["m"] = [x.data_ptr() for x in pick(self.m)]
-                t["v"] = [x.data_ptr() for x in pick(self.v)]
-                if self.state_bits == 8:
-                    t["m_scale"] = [x.data_ptr() for x in pick(self.m_scale)]
-                    t["v_scale"] = [x.data_ptr() for x in pick(self.v_scale)]
-                t["copy"] = [0 if x is None else x.data_ptr() for x in pick(self.copies)]
-                _check(_library().chol_adamw(
-                    len(at), t.ctypes.data, _PARAM[pt], _PARAM[gt], self.state_bits, lr,
-                    self.betas[0], self.betas[1], self.eps, self.steps + 1, _ptr(grad_scale),
-                    _ptr(status), _b._stream_ptr(stream)))
-
+                                 f"a type in {_GRADS[pt]}, got {gt} {tuple(g.shape)}")
+            key = (pt, gt)
+            if key in calls:
+                calls[key].append(i)
+            else:
+                calls[key] = [i]
+        if self._copied:
+            for at in calls.items():
+                for i in at[1]:
+                    c = self.copies[i]
+                    if c is not None and c.dtype != at[0][1]:
+                        raise ValueError(f"copy {i} must have its gradient's dtype {at[0][1]}")
         used = [grad_scale, status]
         if stream is not None:
-            for xs in (self.params, grads, self.copies, self.m, self.v, self.m_scale, self.v_scale):
+            for xs in (params, grads, self.copies, self.m, self.v, self.m_scale, self.v_scale):
                 used += [xs[i] for at in calls.values() for i in at] if xs is not None else []
-        _on(stream, used, call)
+        _on(stream, used, self._run, calls, grads, self.lr if lr is None else float(lr), grad_scale,
+            status, dev)
         self.steps += 1
-        for at in calls.values():
-            torch.autograd.graph.increment_version([self.params[i] for i in at])
+        torch.autograd.graph.increment_version([params[i] for at in calls.values() for i in at])
+
+    def _run(self, calls, grads, lr, grad_scale, status, dev):
+        stream = _current(self.params[0])
+        for (pt, gt), at in calls.items():
+            whole = len(at) == len(self.params)
+            t = self._table.copy() if whole else self._table[at]
+
+            def pointers(xs):
+                return [x.data_ptr() for x in (xs if whole else [xs[i] for i in at])]
+
+            t["param"] = pointers(self.params)
+            t["grad"] = pointers(grads)
+            rc = _library().chol_adamw(
+                len(at), t.ctypes.data, _PARAM[pt], _PARAM[gt], self.state_bits, lr, self.betas[0],
+                self.betas[1], self.eps, self.steps + 1, _ptr(grad_scale), _ptr(status), stream)
+            if rc:
+                _check(rc)

@@ -182,8 +182,10 @@ typedef struct {
  *                 step is skipped and nothing is written (a matrix that was not
  *                 positive definite, a gradient that overflowed).
  * Every multiplication, addition, square root and division is rounded by
- * itself, so equal inputs give equal bits on every path.  No output may overlap
- * another tensor's memory (CHOL_EALIAS).
+ * itself, so equal inputs give equal bits on every path; with 8-bit moments
+ * and parameters other than F64, the amount subtracted from a parameter is
+ * within 4 units of float32 of that instead (the moments are the same bits).
+ * No output may overlap another tensor's memory (CHOL_EALIAS).
  */
 CHOL_API int chol_adamw(int64_t count, const chol_adamw_tensor* tensors, int32_t param_dtype,
                         int32_t grad_dtype, int32_t state_bits, double lr, double beta1,
