@@ -30,6 +30,7 @@
 
 #include <algorithm>
 #include <initializer_list>
+#include <type_traits>
 
 #include "learn.cuh"
 #include "learn.h"
@@ -41,8 +42,8 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kStages = 3;  // tiles of inputs in shared memory: one in use, two on their way
 
-// Inputs reach their thread through shared memory that only it uses, copied
-// asynchronously; single 16-bit elements cannot be, and go to registers.
+// Vectors of inputs reach their thread through shared memory that only it
+// uses, copied asynchronously; single elements go to registers, one tile ahead.
 // Blocks of a cluster: what fits beside the inputs with two blocks on an SM
 // (beyond 8 a cluster is not portable; the device is asked what it schedules).
 template <bool PACKED> struct max_cluster_of {
@@ -56,7 +57,9 @@ template <typename T, int V, bool VEC> struct Hold {
     static constexpr int kPieces = VEC ? 1 : V;
     static constexpr int kWidth = VEC ? V : 1;                     // elements of a piece
     static constexpr int kBytes = kWidth * (int)sizeof(T);
-    static constexpr bool kRing = kBytes >= 4;
+    // (4-byte asynchronous copies measured slower than loads to registers:
+    // 93 us against 55 us for a forward of 20011 x 1001 float32)
+    static constexpr bool kRing = kBytes >= 8;
     static constexpr int kRow = kThreads * V * (int)sizeof(T);     // one row of a tile
     static constexpr int ring_bytes(int ls, bool adj) {
         return kRing ? kStages * (adj ? 4 : 2) * ls * kRow : 0;
@@ -139,21 +142,29 @@ template <typename T, int V> struct Raw {
     static constexpr int kBytes = V * (int)sizeof(T);
     static constexpr int kWords = (kBytes + 3) / 4;
     uint32_t w[kWords];
-    // (ok: else zeros)
+    // (ok: else zeros; by predicate, since a branch for each load costs more
+    // than the load)
     __device__ __forceinline__ void load(const T* p, bool ok) {
 #pragma unroll
         for (int i = 0; i < kWords; ++i) w[i] = 0;
-        if (!ok) return;
         if constexpr (kBytes == 16) {
-            const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
-            w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+            asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+                         "@p ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+                         : "+r"(w[0]), "+r"(w[1]), "+r"(w[2]), "+r"(w[3]) : "l"(p), "r"((int)ok));
         } else if constexpr (kBytes == 8) {
-            const uint2 q = __ldg(reinterpret_cast<const uint2*>(p));
-            w[0] = q.x, w[1] = q.y;
+            asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\t"
+                         "@p ld.global.nc.v2.b32 {%0, %1}, [%2];\n\t}"
+                         : "+r"(w[0]), "+r"(w[1]) : "l"(p), "r"((int)ok));
         } else if constexpr (kBytes == 4) {
-            w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+            asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t"
+                         "@p ld.global.nc.b32 %0, [%1];\n\t}"
+                         : "+r"(w[0]) : "l"(p), "r"((int)ok));
         } else {
-            w[0] = __ldg(reinterpret_cast<const unsigned short*>(p));
+            uint16_t h = 0;
+            asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t"
+                         "@p ld.global.nc.b16 %0, [%1];\n\t}"
+                         : "+h"(h) : "l"(p), "r"((int)ok));
+            w[0] = h;
         }
     }
     __device__ __forceinline__ void load_shared(uint32_t at) {
@@ -273,7 +284,7 @@ __device__ __forceinline__ bool wait_maps(uint64_t* bar, uint32_t parity) {
     return false;
 }
 
-// Steps of a tile that begin or end a sequence, as the tile is walked: the
+// Steps of a tile that begin or end a sequence, as the axis is walked: the
 // sequence's number, else -1.
 struct Marks {
     int* enter;
@@ -281,37 +292,64 @@ struct Marks {
     int* any;  // whether there is one
 };
 
-// Marks of a tile whose steps are [lo, hi) of the time axis, by one warp;
-// row_of gives a step's place in the tile.  Any offsets give marks in the tile
-// and sequences below nseq.
-template <int L, bool ADJ, typename F>
-__device__ __forceinline__ void mark(const LinrecArgs& a, int64_t lo, int64_t hi, Marks m, F row_of) {
-    const int lane = threadIdx.x % 32;
-    for (int i = lane; i < L; i += 32) m.enter[i] = m.leave[i] = -1;
-    if (lane == 0) *m.any = 0;
-    __syncwarp();
-    if (lo >= hi) return;
-    // the first j with offsets[j] >= lo, 32 probes at a time
-    int64_t x = 0, y = a.nseq + 1;
-    while (x < y) {
-        const int64_t step = (y - x + 31) / 32, at = x + lane * step;
-        const bool below = at < y && __ldg(a.offsets + at) < lo;
-        const int n = __popc(__ballot_sync(0xffffffffu, below));
-        if (n == 0) break;
-        y = min(x + n * step, y);
-        x += (n - 1) * step + 1;
+// The sequences' boundaries in the order of the walk, for one warp that marks
+// the tiles of its block.  It holds 32 boundaries in a row, fetched one tile
+// before they are needed; only where more than 30 lie between two of its
+// tiles does it search and wait.  Any offsets give marks in the tile and
+// sequences below nseq.
+template <int L, bool ADJ> struct Marker {
+    int64_t base;   // lane i holds boundary base + i
+    int64_t bound;
+
+    // Boundary j (0 .. nseq) in steps of the walk.
+    static __device__ __forceinline__ int64_t at(const LinrecArgs& a, int64_t j) {
+        return ADJ ? a.time - __ldg(a.offsets + (a.nseq - j)) : __ldg(a.offsets + j);
     }
-    for (int64_t j = x + lane; j <= a.nseq; j += 32) {
-        const int64_t o = __ldg(a.offsets + j);
-        const int64_t before = j > 0 ? __ldg(a.offsets + j - 1) : o;
-        const int64_t after = j < a.nseq ? __ldg(a.offsets + j + 1) : o;
-        if (o > hi) break;
-        int* first = ADJ ? m.leave : m.enter;
-        int* last = ADJ ? m.enter : m.leave;
-        if (o >= lo && o < hi && after > o) first[row_of(o)] = (int)j, *m.any = 1;
-        if (o - 1 >= lo && o - 1 < hi && before < o) last[row_of(o - 1)] = (int)j - 1, *m.any = 1;
+    __device__ __forceinline__ void hold(const LinrecArgs& a, int64_t first) {
+        base = first;
+        const int64_t j = base + threadIdx.x % 32;
+        bound = j < 0 ? INT64_MIN : j <= a.nseq ? at(a, j) : INT64_MAX;
     }
-}
+    // Holds the first boundary that is not below step u, and the one before it.
+    __device__ void find(const LinrecArgs& a, int64_t u) {
+        int64_t x = 0, y = a.nseq + 1;
+        while (x < y) {
+            const int64_t step = (y - x + 31) / 32, j = x + threadIdx.x % 32 * step;
+            const int n = __popc(__ballot_sync(0xffffffffu, j < y && at(a, j) < u));
+            if (n == 0) break;
+            y = min(x + n * step, y);
+            x += (n - 1) * step + 1;
+        }
+        hold(a, x - 1);
+    }
+    // Marks the tile of steps [u, end), and holds what the tile at `next` needs.
+    __device__ void tile(const LinrecArgs& a, int64_t u, int64_t end, int64_t next, Marks m) {
+        const int lane = threadIdx.x % 32;
+        for (int i = lane; i < L; i += 32) m.enter[i] = m.leave[i] = -1;
+        if (lane == 0) *m.any = 0;
+        __syncwarp();
+        if (__shfl_sync(0xffffffffu, bound, 30) < u) find(a, u);
+        for (;;) {
+            const int64_t before = __shfl_up_sync(0xffffffffu, bound, 1);
+            const int64_t after = __shfl_down_sync(0xffffffffu, bound, 1);
+            const int64_t j = base + lane;
+            if (lane >= 1 && lane <= 30 && j >= 0 && j <= a.nseq && bound >= u && bound <= end) {
+                if (j < a.nseq && bound < end && after > bound) {
+                    m.enter[bound - u] = (int)(ADJ ? a.nseq - 1 - j : j);
+                    *m.any = 1;
+                }
+                if (j > 0 && bound > u && before < bound) {
+                    m.leave[bound - 1 - u] = (int)(ADJ ? a.nseq - j : j - 1);
+                    *m.any = 1;
+                }
+            }
+            if (__shfl_sync(0xffffffffu, bound, 30) > end || base + 30 >= a.nseq) break;
+            hold(a, base + 30);
+        }
+        const int below = __popc(__ballot_sync(0xffffffffu, bound < next));
+        if (below > 1) hold(a, base + below - 1);
+    }
+};
 
 // One block of CX * V channels of one row of the batch per cluster; `tiles`
 // is the number of tiles that the cluster's blocks share out, `blocks` the
@@ -355,11 +393,10 @@ linrec_tile_kernel(const LinrecArgs a, const bool comp, const int64_t blocks, co
     // k steps later, as the axis is walked, in elements of an array with this stride
     auto later = [](int k, int64_t stride) { return ADJ ? -(k * stride) : k * stride; };
 
-    // marks of the block's tile that starts at step u, by one warp
+    // the last warp marks the block's tiles
+    Marker<L, ADJ> marker;
     auto mark_tile = [&](int64_t u, int at) {
-        const int64_t last = min(u + L, U);
-        mark<L, ADJ>(a, ADJ ? U - last : u, ADJ ? U - u : last, {marks[at][0], marks[at][1], &marked[at]},
-                     [&](int64_t t) { return (int)((ADJ ? U - 1 - t : t) - u); });
+        marker.tile(a, u, min(u + L, U), u + round_steps, {marks[at][0], marks[at][1], &marked[at]});
     };
     if (threadIdx.x == 0) {
         mbar_init(&arrived[0], 1);
@@ -457,7 +494,10 @@ linrec_tile_kernel(const LinrecArgs a, const bool comp, const int64_t blocks, co
             if constexpr (PACKED) {
                 enter = marks[buf][0], leave = marks[buf][1];
                 if (round == 0) {  // those of later tiles are made while maps are exchanged
-                    if (warp == kWarps - 1) mark_tile(u0 - row0, buf);
+                    if (warp == kWarps - 1) {
+                        marker.hold(a, -1);
+                        mark_tile(u0 - row0, buf);
+                    }
                     __syncthreads();
                 }
                 some = marked[buf];
@@ -467,10 +507,11 @@ linrec_tile_kernel(const LinrecArgs a, const bool comp, const int64_t blocks, co
             bool cut = false;
 #pragma unroll
             for (int v = 0; v < V; ++v) A[v] = 1.0f, H[v] = 0.0f;
+            auto to_map = [&](auto marked_tile) {
 #pragma unroll
             for (int i = 0; i < LS; ++i) {
-                if constexpr (PACKED) {
-                    const int s = some ? enter[row0 + i] : -1;
+                if constexpr (decltype(marked_tile)::value) {
+                    const int s = enter[row0 + i];
                     if (s >= 0) {
                         cut = true;
                         load_state<V, STRIDE>(state_in != nullptr ? state_in + s * a.d + c : nullptr, chans, H);
@@ -493,6 +534,9 @@ linrec_tile_kernel(const LinrecArgs a, const bool comp, const int64_t blocks, co
                 }
                 mul_v<V>(A, A, av[i]);
             }
+            };
+            // (apart: a tile without a mark takes no part of the other's waits)
+            if (PACKED && some) to_map(std::true_type{}); else to_map(std::false_type{});
             if constexpr (!RING) fetch(u0 + round_steps, o + later(round_steps, a.d), 0);
 
             // maps of all steps of the warp up to and with this thread's
@@ -582,15 +626,16 @@ linrec_tile_kernel(const LinrecArgs a, const bool comp, const int64_t blocks, co
             }
             // the steps again, from the state before them
             const int n = steps_at(u0);
+            auto to_steps = [&](auto marked_tile) {
 #pragma unroll
             for (int i = 0; i < LS; ++i) {
                 if (i >= n) break;
                 int64_t leaving = -1;
-                if constexpr (PACKED) {
-                    const int e = some ? enter[row0 + i] : -1;
+                if constexpr (decltype(marked_tile)::value) {
+                    const int e = enter[row0 + i];
                     if (e >= 0) load_state<V, STRIDE>(state_in != nullptr ? state_in + e * a.d + c : nullptr, chans, st);
-                    if (some) leaving = leave[row0 + i];
-                } else {
+                    leaving = leave[row0 + i];
+                } else if constexpr (!PACKED) {
                     if (u0 + i == U - 1) leaving = b;
                 }
                 const int64_t at = o + later(i, a.d);
@@ -614,6 +659,8 @@ linrec_tile_kernel(const LinrecArgs a, const bool comp, const int64_t blocks, co
                 if (leaving >= 0 && state_out != nullptr)
                     store_state<V, STRIDE>(state_out + leaving * a.d + c, chans, st);
             }
+            };
+            if (PACKED && some) to_steps(std::true_type{}); else to_steps(std::false_type{});
             u0 += round_steps;
             o += later(round_steps, a.d);
             stage = stage == kStages - 1 ? 0 : stage + 1;
