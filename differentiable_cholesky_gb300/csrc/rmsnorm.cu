@@ -8,11 +8,12 @@
 // scales come from the unrounded r.  All of it is bound by memory: each row is
 // read once into registers, reduced over its threads, and written.  Three
 // forms of each direction:
-//   pipe: rows whose arrays are all vector-aligned, from 256 columns: a block
-//         keeps several rows on their way to shared memory (bulk copies that
-//         an mbarrier counts) while it works on one, so that loads never stop;
-//   row:  any alignment, up to 8192 columns: a row's threads take single
-//         elements side by side;
+//   pipe: from 256 columns: a block keeps several rows on their way to shared
+//         memory (bulk copies that an mbarrier counts) while it works on one,
+//         so that loads never stop.  Rows that are not vector-aligned are
+//         copied with what lies around them, and worked on element by element;
+//   row:  up to 1024 columns, where the rows are narrow: a warp or a few take
+//         a row's elements side by side;
 //   loop: any width: a block goes over its row two or three times.
 
 #include <algorithm>
@@ -24,7 +25,10 @@
 namespace chol {
 namespace {
 
-constexpr int kThreads = 256;  // of the loop kernels
+constexpr int kThreads = 256;   // of the loop kernels
+// columns from which the pipe form is taken (narrower: 30000 x 64 bf16 8.4 us in
+// rows, 10.3 us piped; 30000 x 200 21.8 against 11.3), and in the adjoint
+constexpr int kPipeFrom = 128, kAdjPipeFrom = 64;
 
 enum OutKind { OUT_MODEL, OUT_E4M3, OUT_I8 };
 
@@ -180,27 +184,32 @@ __global__ void __launch_bounds__(kThreads) rms_norm_adj_loop_kernel(RmsAdjArgs 
     }
 }
 
-// adj_w[j] = sum over the parts: a block takes 32 columns, each of its 32 warps
-// every 32nd part, and the warps' sums are added in order.
-template <typename T>
+// adj_w[j] = sum over the parts: a block takes COLS columns, each of its
+// 1024 / COLS groups of threads every so many parts, and the groups' sums are
+// added in a fixed order (within a warp, then the warps').
+template <typename T, int COLS>
 __global__ void __launch_bounds__(1024)
 column_sum_kernel(const float* __restrict__ work, int64_t parts, int64_t d, T* __restrict__ out) {
-    __shared__ float sums[32][33];
+    __shared__ float sums[32][COLS];
     pdl_wait();
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const int64_t j = (int64_t)blockIdx.x * 32 + lane;
+    const int c = threadIdx.x % COLS, warp = threadIdx.x / 32;
+    const int64_t j = (int64_t)blockIdx.x * COLS + c;
     float s = 0.0f;
     if (j < d) {
-#pragma unroll 8
-        for (int64_t p = warp; p < parts; p += 32) s += work[p * d + j];
+#pragma unroll 4
+        for (int64_t p = threadIdx.x / COLS; p < parts; p += 1024 / COLS) s += work[p * d + j];
     }
-    sums[warp][lane] = s;
+#pragma unroll
+    for (int o = COLS; o < 32; o *= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (threadIdx.x % 32 < COLS) sums[warp][c] = s;
     __syncthreads();
-    if (warp != 0 || j >= d) return;
+    if (warp != 0) return;
     s = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 32; ++w) s += sums[w][lane];
-    out[j] = from_f32<T>(s);
+    for (int w = 0; w < 32; w += 32 / COLS) s += sums[w + threadIdx.x / COLS][c];
+#pragma unroll
+    for (int o = COLS; o < 32; o *= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (threadIdx.x < COLS && j < d) out[j] = from_f32<T>(s);
 }
 
 // ---------------------------------------------------------------------------
@@ -275,6 +284,7 @@ __device__ __forceinline__ uint32_t row_max(uint32_t x, uint32_t* tmp, int warp,
 // pipe: one row at a time, the next ones on their way
 // ---------------------------------------------------------------------------
 constexpr int kMaxStages = 6;
+constexpr int kMaxGroups = 128;  // 16384 columns
 
 struct Pipe {
     int threads, stages;
@@ -282,22 +292,113 @@ struct Pipe {
     size_t bytes;
 };
 
-// The copies of a block's rows into a ring of stages.  ROWS arrays of
-// `bytes[i]` a row; stage s begins at ring + s * stage_bytes.
-template <int ARRAYS>
+// The copies of a block's rows into a ring of stages: the rows of ARRAYS
+// arrays, one behind another in a stage.  Rows that are not aligned (VEC
+// false) are copied with what lies around them up to 16-byte boundaries, so
+// that they begin `shift` bytes into their place; the first and the last row,
+// around which there may be nothing, are not copied but read where they are.
+template <int ARRAYS, bool VEC>
 struct RowCopies {
-    const char* at[ARRAYS];   // the array's row `first`
-    int64_t step[ARRAYS];     // bytes between rows
-    uint32_t bytes[ARRAYS];
-    uint32_t total;           // of a stage
+    const char* at[ARRAYS];  // the first row
+    int64_t step[ARRAYS];    // bytes between rows
+    uint32_t bytes[ARRAYS];  // of a row
+    int64_t rows;
+
+    static __host__ __device__ __forceinline__ uint32_t place(uint32_t bytes) {
+        return VEC || bytes == 0 ? bytes : (bytes + 30 + 15) / 16 * 16;
+    }
+    __device__ __forceinline__ uint32_t stage_bytes() const {
+        uint32_t n = 0;
+#pragma unroll
+        for (int i = 0; i < ARRAYS; ++i) n += place(bytes[i]);
+        return n;
+    }
+    __device__ __forceinline__ bool copied(int64_t row) const { return VEC || (row > 0 && row < rows - 1); }
     __device__ __forceinline__ void issue(char* stage, uint64_t* bar, int64_t row) const {
+        const char* from[ARRAYS];
+        uint32_t n[ARRAYS], total = 0;
+#pragma unroll
+        for (int i = 0; i < ARRAYS; ++i) {
+            from[i] = at[i] + row * step[i];
+            n[i] = copied(row) ? bytes[i] : 0;
+            if (!VEC && n[i] > 0) {
+                const uint32_t shift = (uint32_t)(reinterpret_cast<uintptr_t>(from[i]) & 15);
+                from[i] -= shift;
+                n[i] = (n[i] + shift + 15) / 16 * 16;
+            }
+            total += n[i];
+        }
         mbar_arrive_expect_tx(bar, total);
         uint32_t off = 0;
 #pragma unroll
         for (int i = 0; i < ARRAYS; ++i) {
-            if (bytes[i] > 0) bulk_load(stage + off, at[i] + row * step[i], bytes[i], bar);
-            off += bytes[i];
+            if (n[i] > 0) bulk_load(stage + off, from[i], n[i], bar);
+            off += place(bytes[i]);
         }
+    }
+    // Array i's row in its stage, or where it is.
+    __device__ __forceinline__ const char* row_of(const char* stage, int i, int64_t row) const {
+        const char* from = at[i] + row * step[i];
+        if (!copied(row)) return from;
+#pragma unroll
+        for (int k = 0; k < i; ++k) stage += place(bytes[k]);
+        return stage + (VEC ? 0 : (uint32_t)(reinterpret_cast<uintptr_t>(from) & 15));
+    }
+};
+
+// Piece k of a thread's part of a row: eight consecutive columns (VEC), or
+// eight that lie the block's threads apart.  column(k, i) of piece k's i-th.
+template <bool VEC> __device__ __forceinline__ int column(int k, int i) {
+    return VEC ? (k * blockDim.x + threadIdx.x) * 8 + i : (k * 8 + i) * blockDim.x + threadIdx.x;
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void get_piece(const char* row, int k, int d, float (&f)[8]) {
+    if constexpr (VEC) {
+        Eight<T> q;
+        q.load_shared(row + column<VEC>(k, 0) * sizeof(T));
+        q.get(f);
+    } else {
+        // columns beyond the row read its last one and count as zero: no load
+        // hangs on a branch
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            f[i] = to_f32(reinterpret_cast<const T*>(row)[min(column<VEC>(k, i), d - 1)]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = column<VEC>(k, i) < d ? f[i] : 0.0f;
+    }
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void put_piece(T* row, int k, int d, const float (&f)[8]) {
+    if constexpr (VEC) {
+        Eight<T> q;
+        q.set(f);
+        q.store(row + column<VEC>(k, 0));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (column<VEC>(k, i) < d) row[column<VEC>(k, i)] = from_f32<T>(f[i]);
+    }
+}
+// Elements of a thread's columns that it keeps (packed where they can be): the
+// weights for all rows, a row's adj_r until it is added.
+template <typename T, bool VEC> struct Kept {
+    Eight<T> q;
+    __device__ __forceinline__ void load(const T* w, int k, int) { q.load(w + column<VEC>(k, 0)); }
+    __device__ __forceinline__ void take(const char* row, int k, int) {
+        q.load_shared(row + column<VEC>(k, 0) * sizeof(T));
+    }
+    __device__ __forceinline__ void get(float (&f)[8]) const { q.get(f); }
+};
+template <typename T> struct Kept<T, false> {
+    float x[8];
+    __device__ __forceinline__ void load(const T* w, int k, int d) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = column<false>(k, i) < d ? to_f32(w[column<false>(k, i)]) : 0.0f;
+    }
+    __device__ __forceinline__ void take(const char* row, int k, int d) { get_piece<T, false>(row, k, d, x); }
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = x[i];
     }
 };
 
@@ -307,55 +408,57 @@ __device__ __forceinline__ float stage_ready(uint64_t* bar, uint32_t parity, boo
     return lost ? __int_as_float(0x7fffffff) : 0.0f;
 }
 
-// K vectors of eight columns a thread.
-template <typename T, typename R, int OUT, int K>
+// K pieces of eight columns a thread.
+template <typename T, typename R, int OUT, int K, bool VEC>
 __global__ void __launch_bounds__(512) rms_norm_pipe_kernel(const RmsArgs a, const int stages) {
     extern __shared__ __align__(128) char ring[];
     __shared__ uint64_t bars[kMaxStages];
     __shared__ float tmp[2][32];
     __shared__ uint32_t tmp_max[2][32];
+    constexpr bool kTops = OUT != OUT_MODEL && !VEC;  // groups whose columns several warps hold
+    __shared__ uint32_t tops[kTops ? kMaxGroups : 1];
+    __shared__ float inverses[kTops ? kMaxGroups : 1];
     const int d = (int)a.d, nt = blockDim.x, warp = threadIdx.x / 32, warps = nt / 32;
+    const int groups = (d + 127) / 128;
     const bool has_res = a.res != nullptr;
-    RowCopies<2> copies;
+    RowCopies<2, VEC> copies;
     copies.at[0] = static_cast<const char*>(a.x), copies.step[0] = a.ldx * (int64_t)sizeof(T);
     copies.at[1] = static_cast<const char*>(a.res), copies.step[1] = a.ldr * (int64_t)sizeof(R);
     copies.bytes[0] = d * (uint32_t)sizeof(T), copies.bytes[1] = has_res ? d * (uint32_t)sizeof(R) : 0;
-    copies.total = copies.bytes[0] + copies.bytes[1];
+    copies.rows = a.rows;
+    const size_t stage_bytes = copies.stage_bytes();
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; ++s) mbar_init(&bars[s], 1);
         fence_mbar_init();
         for (int s = 0; s < stages; ++s) {
             const int64_t row = blockIdx.x + (int64_t)s * gridDim.x;
-            if (row < a.rows) copies.issue(ring + (size_t)s * copies.total, &bars[s], row);
+            if (row < a.rows) copies.issue(ring + s * stage_bytes, &bars[s], row);
         }
     }
-    Eight<T> w[K];
+    Kept<T, VEC> w[K];
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int j = (k * nt + threadIdx.x) * 8;
-        if (a.w != nullptr && j < d) w[k].load(static_cast<const T*>(a.w) + j);
-    }
+    for (int k = 0; k < K; ++k)
+        if (a.w != nullptr && column<VEC>(k, 0) < d) w[k].load(static_cast<const T*>(a.w), k, d);
+    if constexpr (kTops)
+        for (int g = threadIdx.x; g < groups; g += nt) tops[g] = 0;
     __syncthreads();
     int stage = 0, turn = 0;
     uint32_t parity = 0;
     bool lost = false;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
-        const char* at = ring + (size_t)stage * copies.total;
-        const float poison = stage_ready(&bars[stage], parity, lost);
-        float v[K][8], ss = poison;
+        const char* at = ring + stage * stage_bytes;
+        float ss = stage_ready(&bars[stage], parity, lost);
+        const char* x = copies.row_of(at, 0, row);
+        const char* res = copies.row_of(at, 1, row);
+        float v[K][8];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int j = (k * nt + threadIdx.x) * 8;
             fill_v<8>(v[k], 0.0f);
-            if (j < d) {
-                Eight<T> q;
-                q.load_shared(at + j * sizeof(T));
-                q.get(v[k]);
+            if (column<VEC>(k, 0) < d) {
+                get_piece<T, VEC>(x, k, d, v[k]);
                 if (has_res) {
-                    Eight<R> p;
                     float f[8];
-                    p.load_shared(at + copies.bytes[0] + j * sizeof(R));
-                    p.get(f);
+                    get_piece<R, VEC>(res, k, d, f);
                     add_v<8>(v[k], v[k], f);
                 }
             }
@@ -371,7 +474,7 @@ __global__ void __launch_bounds__(512) rms_norm_pipe_kernel(const RmsArgs a, con
         // every thread has its row in registers: the stage is free
         if (threadIdx.x == 0) {
             const int64_t next = row + (int64_t)stages * gridDim.x;
-            if (next < a.rows) copies.issue(ring + (size_t)stage * copies.total, &bars[stage], next);
+            if (next < a.rows) copies.issue(ring + stage * stage_bytes, &bars[stage], next);
         }
         if (++stage == stages) stage = 0, parity ^= 1;
         const float rstd = rsqrtf(ss / (float)d + a.eps);
@@ -379,25 +482,17 @@ __global__ void __launch_bounds__(512) rms_norm_pipe_kernel(const RmsArgs a, con
         uint32_t row_top = 0;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int j = (k * nt + threadIdx.x) * 8;
-            if (j < d && a.r != nullptr) {
-                Eight<R> p;
-                p.set(v[k]);
-                p.store(static_cast<R*>(a.r) + row * a.d + j);
-            }
+            const bool here = column<VEC>(k, 0) < d;
+            if (here && a.r != nullptr) put_piece<R, VEC>(static_cast<R*>(a.r) + row * a.d, k, d, v[k]);
             scale_v<8>(v[k], v[k], rstd);
-            if (a.w != nullptr && j < d) {
+            if (a.w != nullptr && here) {
                 float f[8];
                 w[k].get(f);
                 mul_v<8>(v[k], v[k], f);
             }
             if constexpr (OUT == OUT_MODEL) {
-                if (j < d) {
-                    Eight<T> q;
-                    q.set(v[k]);
-                    q.store(static_cast<T*>(a.y) + row * a.d + j);
-                }
-            } else {
+                if (here) put_piece<T, VEC>(static_cast<T*>(a.y) + row * a.d, k, d, v[k]);
+            } else if constexpr (VEC) {
                 uint32_t top = 0;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) top = max(top, abs_bits(v[k][i]));
@@ -408,9 +503,22 @@ __global__ void __launch_bounds__(512) rms_norm_pipe_kernel(const RmsArgs a, con
 #pragma unroll
                     for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
                     const float scale = scale_of<OUT>(top);
-                    if (j < d) {
-                        if (threadIdx.x % 16 == 0) a.scale[row * ((d + 127) / 128) + j / 128] = scale;
+                    const int j = column<VEC>(k, 0);
+                    if (here) {
+                        if (threadIdx.x % 16 == 0) a.scale[row * groups + j / 128] = scale;
                         store_codes<OUT>(static_cast<uint8_t*>(a.y) + row * a.d + j, v[k], inverse_of(scale));
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int j = column<VEC>(k, i), j0 = j - threadIdx.x % 32;
+                    const uint32_t top = j < d ? abs_bits(v[k][i]) : 0u;
+                    if (a.group == 0) {
+                        row_top = max(row_top, top);
+                    } else {  // the 32 columns of a warp are of one group
+                        const uint32_t most = warp_max(top);
+                        if (threadIdx.x % 32 == 0 && j0 < d) atomicMax(&tops[j0 / 128], most);
                     }
                 }
             }
@@ -419,45 +527,69 @@ __global__ void __launch_bounds__(512) rms_norm_pipe_kernel(const RmsArgs a, con
             if (a.group == 0) {
                 const float scale = scale_of<OUT>(row_max(row_top, tmp_max[turn], warp, warps));
                 if (threadIdx.x == 0) a.scale[row] = scale;
+                const float inv = inverse_of(scale);
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
-                    const int j = (k * nt + threadIdx.x) * 8;
-                    if (j < d)
-                        store_codes<OUT>(static_cast<uint8_t*>(a.y) + row * a.d + j, v[k], inverse_of(scale));
+                    uint8_t* y = static_cast<uint8_t*>(a.y) + row * a.d;
+                    if constexpr (VEC) {
+                        if (column<VEC>(k, 0) < d) store_codes<OUT>(y + column<VEC>(k, 0), v[k], inv);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (column<VEC>(k, i) < d) y[column<VEC>(k, i)] = to_code8<OUT>(v[k][i] * inv);
+                    }
                 }
+            } else if constexpr (!VEC) {
+                __syncthreads();
+                for (int g = threadIdx.x; g < groups; g += nt) {
+                    const float scale = scale_of<OUT>(tops[g]);
+                    a.scale[row * groups + g] = scale;
+                    inverses[g] = inverse_of(scale);
+                    tops[g] = 0;
+                }
+                __syncthreads();
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int j = column<VEC>(k, i);
+                        if (j < d)
+                            static_cast<uint8_t*>(a.y)[row * a.d + j] = to_code8<OUT>(v[k][i] * inverses[j / 128]);
+                    }
+                if (warps == 1) __syncwarp();  // (else the next row's sum is a barrier)
             }
         }
     }
 }
 
-template <typename T, typename R, int K>
+template <typename T, typename R, int K, bool VEC>
 __global__ void __launch_bounds__(512) rms_norm_adj_pipe_kernel(const RmsAdjArgs a, const int stages) {
     extern __shared__ __align__(128) char ring[];
     __shared__ uint64_t bars[kMaxStages];
     __shared__ float tmp[2][32];
     const int d = (int)a.d, nt = blockDim.x, warp = threadIdx.x / 32, warps = nt / 32;
     const bool has_dr = a.adj_r != nullptr;
-    RowCopies<3> copies;
+    RowCopies<3, VEC> copies;
     copies.at[0] = static_cast<const char*>(a.adj_y), copies.step[0] = a.ldy * (int64_t)sizeof(T);
     copies.at[1] = static_cast<const char*>(a.r), copies.step[1] = a.ldr * (int64_t)sizeof(R);
     copies.at[2] = static_cast<const char*>(a.adj_r), copies.step[2] = a.d * (int64_t)sizeof(R);
     copies.bytes[0] = d * (uint32_t)sizeof(T), copies.bytes[1] = d * (uint32_t)sizeof(R);
     copies.bytes[2] = has_dr ? copies.bytes[1] : 0;
-    copies.total = copies.bytes[0] + copies.bytes[1] + copies.bytes[2];
+    copies.rows = a.rows;
+    const size_t stage_bytes = copies.stage_bytes();
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; ++s) mbar_init(&bars[s], 1);
         fence_mbar_init();
         for (int s = 0; s < stages; ++s) {
             const int64_t row = blockIdx.x + (int64_t)s * gridDim.x;
-            if (row < a.rows) copies.issue(ring + (size_t)s * copies.total, &bars[s], row);
+            if (row < a.rows) copies.issue(ring + s * stage_bytes, &bars[s], row);
         }
     }
-    Eight<T> w[K];
+    Kept<T, VEC> w[K];
     float dw[K][8];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const int j = (k * nt + threadIdx.x) * 8;
-        if (a.w != nullptr && j < d) w[k].load(static_cast<const T*>(a.w) + j);
+        if (a.w != nullptr && column<VEC>(k, 0) < d) w[k].load(static_cast<const T*>(a.w), k, d);
         fill_v<8>(dw[k], 0.0f);
     }
     __syncthreads();
@@ -465,22 +597,20 @@ __global__ void __launch_bounds__(512) rms_norm_adj_pipe_kernel(const RmsAdjArgs
     uint32_t parity = 0;
     bool lost = false;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
-        const char* at = ring + (size_t)stage * copies.total;
+        const char* at = ring + stage * stage_bytes;
         const float rstd = a.rstd[row];
         float c = stage_ready(&bars[stage], parity, lost);
+        const char* dy = copies.row_of(at, 0, row);
+        const char* r = copies.row_of(at, 1, row);
+        const char* dr = copies.row_of(at, 2, row);
         float u[K][8], n[K][8];
-        Eight<R> add[K];
+        Kept<R, VEC> add[K];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int j = (k * nt + threadIdx.x) * 8;
-            if (j >= d) continue;
-            Eight<T> q;
-            q.load_shared(at + j * sizeof(T));
-            q.get(u[k]);
-            Eight<R> p;
-            p.load_shared(at + copies.bytes[0] + j * sizeof(R));
-            p.get(n[k]);
-            if (has_dr) add[k].load_shared(at + copies.bytes[0] + copies.bytes[1] + j * sizeof(R));
+            if (column<VEC>(k, 0) >= d) continue;
+            get_piece<T, VEC>(dy, k, d, u[k]);
+            get_piece<R, VEC>(r, k, d, n[k]);
+            if (has_dr) add[k].take(dr, k, d);
             scale_v<8>(n[k], n[k], rstd);
             fma_v<8>(dw[k], u[k], n[k], dw[k]);
             if (a.w != nullptr) {
@@ -499,14 +629,13 @@ __global__ void __launch_bounds__(512) rms_norm_adj_pipe_kernel(const RmsAdjArgs
         }
         if (threadIdx.x == 0) {
             const int64_t next = row + (int64_t)stages * gridDim.x;
-            if (next < a.rows) copies.issue(ring + (size_t)stage * copies.total, &bars[stage], next);
+            if (next < a.rows) copies.issue(ring + stage * stage_bytes, &bars[stage], next);
         }
         if (++stage == stages) stage = 0, parity ^= 1;
         c /= (float)d;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int j = (k * nt + threadIdx.x) * 8;
-            if (j >= d) continue;
+            if (column<VEC>(k, 0) >= d) continue;
             // rstd (u - n c) + adj_r
             float f[8], s[8];
             fill_v<8>(f, -c);
@@ -515,28 +644,26 @@ __global__ void __launch_bounds__(512) rms_norm_adj_pipe_kernel(const RmsAdjArgs
             fill_v<8>(f, 0.0f);
             if (has_dr) add[k].get(f);
             fma_v<8>(u[k], u[k], s, f);
-            if (a.adj_in != nullptr) {
-                Eight<R> p;
-                p.set(u[k]);
-                p.store(static_cast<R*>(a.adj_in) + row * a.d + j);
-            }
-            if (a.adj_x != nullptr) {
-                Eight<T> q;
-                q.set(u[k]);
-                q.store(static_cast<T*>(a.adj_x) + row * a.d + j);
-            }
+            if (a.adj_in != nullptr) put_piece<R, VEC>(static_cast<R*>(a.adj_in) + row * a.d, k, d, u[k]);
+            if (a.adj_x != nullptr) put_piece<T, VEC>(static_cast<T*>(a.adj_x) + row * a.d, k, d, u[k]);
         }
     }
     if (a.adj_w == nullptr) return;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const int j = (k * nt + threadIdx.x) * 8;
-        if (j >= d) continue;
-        float* part = a.work + (int64_t)blockIdx.x * a.d + j;
+        float* part = a.work + (int64_t)blockIdx.x * a.d;
+        if constexpr (VEC) {
+            const int j = column<VEC>(k, 0);
+            if (j >= d) continue;
 #pragma unroll
-        for (int i = 0; i < 8; i += 4)
-            *reinterpret_cast<float4*>(part + i) =
-                make_float4(dw[k][i], dw[k][i + 1], dw[k][i + 2], dw[k][i + 3]);
+            for (int i = 0; i < 8; i += 4)
+                *reinterpret_cast<float4*>(part + j + i) =
+                    make_float4(dw[k][i], dw[k][i + 1], dw[k][i + 2], dw[k][i + 3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (column<VEC>(k, i) < d) part[column<VEC>(k, i)] = dw[k][i];
+        }
     }
 }
 
@@ -669,10 +796,12 @@ Pipe pipe_of(int64_t rows, int64_t vecs, int64_t bytes, int k, int64_t blocks) {
     p.threads = (int)((vecs + k * 32 - 1) / (k * 32)) * 32;
     if (p.threads > 512) return p;
     const int sms = device_sm_count();
-    p.blocks = (unsigned)std::min(rows, blocks);
-    const int64_t share = std::max<int64_t>(1, (p.blocks + sms - 1) / sms);
-    const int64_t fits = (216 * 1024 / share - 2048) / bytes;
-    p.stages = (int)std::min<int64_t>(fits, kMaxStages);
+    for (;; blocks = std::max<int64_t>(sms, blocks / 2)) {  // fewer where rows are too long
+        p.blocks = (unsigned)std::min(rows, blocks);
+        const int64_t share = (p.blocks + sms - 1) / sms;
+        p.stages = (int)std::min<int64_t>((216 * 1024 / share - 2048) / bytes, kMaxStages);
+        if (p.stages >= 2 || share == 1) break;
+    }
     p.stages = (int)std::min<int64_t>(p.stages, std::max<int64_t>(2, (rows + p.blocks - 1) / p.blocks));
     p.bytes = (size_t)p.stages * bytes;
     return p;
@@ -686,14 +815,16 @@ cudaError_t launch_pipe(K kern, const Pipe& p, const A& a, std::atomic<uint64_t>
     return cudaGetLastError();
 }
 
-template <typename T, typename R, int OUT, int K>
+template <typename T, typename R, int OUT, int K, bool VEC>
 cudaError_t try_pipe(const RmsArgs& a, int64_t per_sm, bool* ran, cudaStream_t stream) {
     static std::atomic<uint64_t> set{0};
-    const int64_t bytes = a.d * (int64_t)(sizeof(T) + (a.res != nullptr ? sizeof(R) : 0));
-    const Pipe p = pipe_of(a.rows, a.d / 8, bytes, K, device_sm_count() * per_sm);
+    using Copies = RowCopies<2, VEC>;
+    const int64_t bytes = (int64_t)Copies::place(a.d * sizeof(T)) +
+                          Copies::place(a.res != nullptr ? a.d * sizeof(R) : 0);
+    const Pipe p = pipe_of(a.rows, (a.d + 7) / 8, bytes, K, device_sm_count() * per_sm);
     *ran = p.stages >= 2;
     if (!*ran) return cudaSuccess;
-    return launch_pipe(rms_norm_pipe_kernel<T, R, OUT, K>, p, a, set, stream);
+    return launch_pipe(rms_norm_pipe_kernel<T, R, OUT, K, VEC>, p, a, set, stream);
 }
 
 template <typename T, typename R, int OUT, int E>
@@ -724,22 +855,29 @@ cudaError_t launch_rows(const RmsArgs& a, cudaStream_t stream) {
 template <typename T, typename R, int OUT>
 cudaError_t launch_out(const RmsArgs& a, cudaStream_t stream) {
     const size_t ys = OUT == OUT_MODEL ? sizeof(T) : 1;
-    const bool vec = a.d % 8 == 0 && a.d >= 256 && rows_aligned(a.x, a.ldx, sizeof(T)) &&
+    const bool vec = a.d % 8 == 0 && rows_aligned(a.x, a.ldx, sizeof(T)) &&
                      rows_aligned(a.res, a.ldr, sizeof(R)) && rows_aligned(a.r, a.d, sizeof(R)) &&
                      rows_aligned(a.w, 8, sizeof(T)) && aligned(a.y, 8 * ys);
-    if (vec) {
+    if (a.d >= kPipeFrom && a.d <= kMaxGroups * 128) {
         bool ran = false;
         const int64_t per_sm = std::max<int64_t>(2, std::min<int64_t>(16, 8192 / a.d));
-        // one vector a thread where there are few rows or narrow ones
-        const bool few = a.rows <= device_sm_count() || a.d <= 2048;
         cudaError_t e = cudaSuccess;
-        if (few) e = try_pipe<T, R, OUT, 1>(a, per_sm, &ran, stream);
-        if (!ran) e = try_pipe<T, R, OUT, 2>(a, per_sm, &ran, stream);
-        if (!ran) e = try_pipe<T, R, OUT, 4>(a, per_sm, &ran, stream);
+        if (vec) {
+            // one vector a thread where there are few rows or narrow ones
+            const bool few = a.rows <= device_sm_count() || a.d <= 2048;
+            if (few) e = try_pipe<T, R, OUT, 1, true>(a, per_sm, &ran, stream);
+            if (!ran) e = try_pipe<T, R, OUT, 2, true>(a, per_sm, &ran, stream);
+            if (!ran) e = try_pipe<T, R, OUT, 4, true>(a, per_sm, &ran, stream);
+        } else {
+            // more and smaller blocks: 8192 x 4095 bf16 66 us, with one piece a
+            // thread and half the blocks 78 us; but 8-bit output, which works
+            // longer on a row: 16384 x 1135 float32 94 us against 62 us
+            if (OUT != OUT_MODEL) e = try_pipe<T, R, OUT, 1, false>(a, per_sm, &ran, stream);
+            if (!ran) e = try_pipe<T, R, OUT, 2, false>(a, 2 * per_sm, &ran, stream);
+        }
         if (ran) return e;
     }
     if (a.d <= 1024) return launch_rows<T, R, OUT, 4>(a, stream);
-    if (a.d <= 8192) return launch_rows<T, R, OUT, 8>(a, stream);
     const unsigned blocks = (unsigned)std::min<int64_t>(a.rows, 1 << 20);
     rms_norm_loop_kernel<T, R, OUT><<<blocks, kThreads, 0, stream>>>(a);
     return cudaGetLastError();
@@ -752,14 +890,17 @@ cudaError_t launch_fwd(const RmsArgs& a, int32_t y_dtype, cudaStream_t stream) {
     return launch_out<T, R, OUT_MODEL>(a, stream);
 }
 
-template <typename T, typename R, int K>
-cudaError_t try_adj_pipe(const RmsAdjArgs& a, int64_t parts, bool* ran, cudaStream_t stream) {
+template <typename T, typename R, int K, bool VEC>
+cudaError_t try_adj_pipe(const RmsAdjArgs& a, int64_t* parts, bool* ran, cudaStream_t stream) {
     static std::atomic<uint64_t> set{0};
-    const int64_t bytes = a.d * (int64_t)(sizeof(T) + sizeof(R) * (a.adj_r != nullptr ? 2 : 1));
-    const Pipe p = pipe_of(a.rows, a.d / 8, bytes, K, parts);
+    using Copies = RowCopies<3, VEC>;
+    const int64_t bytes = (int64_t)Copies::place(a.d * sizeof(T)) + Copies::place(a.d * sizeof(R)) +
+                          Copies::place(a.adj_r != nullptr ? a.d * sizeof(R) : 0);
+    const Pipe p = pipe_of(a.rows, (a.d + 7) / 8, bytes, K, *parts);
     *ran = p.stages >= 2;
     if (!*ran) return cudaSuccess;
-    return launch_pipe(rms_norm_adj_pipe_kernel<T, R, K>, p, a, set, stream);
+    *parts = p.blocks;
+    return launch_pipe(rms_norm_adj_pipe_kernel<T, R, K, VEC>, p, a, set, stream);
 }
 
 template <typename T, typename R, int E>
@@ -773,30 +914,38 @@ cudaError_t launch_adj_rows(const RmsAdjArgs& a, int64_t parts, cudaStream_t str
 
 template <typename T, typename R>
 cudaError_t launch_adj(const RmsAdjArgs& a, cudaStream_t stream) {
-    const int64_t parts = adj_w_parts(a.rows, a.d);
-    const bool vec = a.d % 8 == 0 && a.d >= 256 && rows_aligned(a.adj_y, a.ldy, sizeof(T)) &&
+    int64_t parts = adj_w_parts(a.rows, a.d);
+    const bool vec = a.d % 8 == 0 && rows_aligned(a.adj_y, a.ldy, sizeof(T)) &&
                      rows_aligned(a.r, a.ldr, sizeof(R)) && rows_aligned(a.adj_r, a.d, sizeof(R)) &&
                      rows_aligned(a.adj_in, a.d, sizeof(R)) && rows_aligned(a.adj_x, a.d, sizeof(T)) &&
                      rows_aligned(a.w, 8, sizeof(T));
     cudaError_t e = cudaSuccess;
     bool ran = false;
-    if (vec) {
-        if (a.d <= 4096) e = try_adj_pipe<T, R, 1>(a, parts, &ran, stream);
-        if (!ran && e == cudaSuccess) e = try_adj_pipe<T, R, 2>(a, parts, &ran, stream);
+    if (a.d >= kAdjPipeFrom) {
+        if (a.d <= 4096)
+            e = vec ? try_adj_pipe<T, R, 1, true>(a, &parts, &ran, stream)
+                    : try_adj_pipe<T, R, 1, false>(a, &parts, &ran, stream);
+        if (!ran && e == cudaSuccess && a.d <= 8192)
+            e = vec ? try_adj_pipe<T, R, 2, true>(a, &parts, &ran, stream)
+                    : try_adj_pipe<T, R, 2, false>(a, &parts, &ran, stream);
     }
-    if (!ran) {
+    if (!ran && e == cudaSuccess) {
         if (a.d <= 1024) {
             e = launch_adj_rows<T, R, 4>(a, parts, stream);
-        } else if (a.d <= 8192) {
-            e = launch_adj_rows<T, R, 8>(a, parts, stream);
         } else {
             rms_norm_adj_loop_kernel<T, R><<<(unsigned)parts, kThreads, 0, stream>>>(a);
             e = cudaGetLastError();
         }
     }
     if (e != cudaSuccess || a.adj_w == nullptr) return e;
-    return launch_pdl(column_sum_kernel<T>, dim3((unsigned)((a.d + 31) / 32)), dim3(1024), 0, stream,
-                      static_cast<const float*>(a.work), parts, a.d, static_cast<T*>(a.adj_w));
+    // fewer columns a block where there are few, to have blocks for every SM
+    const float* work = a.work;
+    T* out = static_cast<T*>(a.adj_w);
+    return a.d >= 4096
+               ? launch_pdl(column_sum_kernel<T, 32>, dim3((unsigned)((a.d + 31) / 32)), dim3(1024), 0,
+                            stream, work, parts, a.d, out)
+               : launch_pdl(column_sum_kernel<T, 8>, dim3((unsigned)((a.d + 7) / 8)), dim3(1024), 0,
+                            stream, work, parts, a.d, out);
 }
 
 }  // namespace
