@@ -3,7 +3,9 @@
 Each ``csrc/*.cu`` translation unit is compiled by its own ``nvcc`` process in
 parallel, then linked with ``nvcc -shared``.  The CUDA runtime is linked
 statically, so the library needs nothing on the loader path.  Sources are
-rebuilt only when newer than the library (or with ``force=True``).
+rebuilt only when newer than the library (or with ``force=True``).  Beside it,
+g++ compiles the native argument marshalling of :mod:`.learn` against the
+installed torch.
 """
 from __future__ import annotations
 
@@ -20,6 +22,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_NAME = "libchol_gb300.so"
 LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
+MARSHAL_SOURCE = os.path.join(CSRC, "marshal.cpp")
+MARSHAL_PATH = os.path.join(BUILD_DIR, "_marshal.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC",
@@ -52,10 +56,58 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def marshal_up_to_date() -> bool:
+    if not os.path.exists(MARSHAL_PATH):
+        return False
+    t = os.path.getmtime(MARSHAL_PATH)
+    return all(os.path.getmtime(p) <= t for p in (MARSHAL_SOURCE, __file__,
+                                                  os.path.join(INCLUDE, "chol_learn.h")))
+
+
+def _start_marshal():
+    """Starts the compiler on the native marshalling of :mod:`.learn`, against
+    the torch that is installed (host code only)."""
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    tmp = MARSHAL_PATH + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-I", os.path.join(base, "include"),
+           "-I", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           "-I", os.path.join(cuda, "include"), MARSHAL_SOURCE, "-o", tmp,
+           "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    return tmp, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+
+
+def _finish_marshal(started):
+    """Without it (no torch headers, say) :mod:`.learn` marshals in Python."""
+    tmp, p = started
+    out, _ = p.communicate()
+    if p.returncode == 0:
+        os.replace(tmp, MARSHAL_PATH)
+        return
+    if os.path.exists(MARSHAL_PATH):
+        os.remove(MARSHAL_PATH)
+    print("native marshalling not built (calls go through Python):\n"
+          + out.decode(errors="replace")[-2000:], file=sys.stderr)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    marshal = None if not force and marshal_up_to_date() else _start_marshal()
+    try:
+        return _build_library(force, verbose)
+    finally:
+        if marshal is not None:
+            _finish_marshal(marshal)
+
+
+def _build_library(force: bool, verbose: bool) -> str:
     if not force and up_to_date():
         return LIB_PATH
-    os.makedirs(BUILD_DIR, exist_ok=True)
     exe = nvcc()
     procs = []
     objs = []

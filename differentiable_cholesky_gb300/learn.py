@@ -13,11 +13,13 @@ optimiser behind its adjoint.
 As in :mod:`.binding`, this is argument marshalling only: every step runs in
 the library's CUDA kernels, and there is no fallback.  Work goes to the
 current stream, or to ``stream``; the caller orders that stream behind what
-made the inputs.
+made the inputs.  The usual calls on the current stream are marshalled natively
+(``csrc/marshal.cpp``); what that does not take comes back to the checks here.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 
 import numpy as np
 import torch
@@ -34,6 +36,23 @@ _CODES = {"e4m3": (CHOL_E4M3, torch.float8_e4m3fn), "int8": (CHOL_I8, torch.int8
 BLOCK = 256  # moments of AdamW that share a scale
 
 _lib = None
+_native = None  # the module of marshal.cpp; False where it is not there
+
+
+def _load_native():
+    """The native marshalling, bound to the loaded library's entry points."""
+    global _native
+    lib = _library()
+    _native = False
+    if _b._build.marshal_up_to_date():
+        spec = importlib.util.spec_from_file_location("_marshal", _b._build.MARSHAL_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in
+                      (lib.chol_rms_norm, lib.chol_rms_norm_adj, lib.chol_rms_norm_adj_workspace,
+                       lib.chol_linrec, lib.chol_linrec_adj, lib.chol_adamw)))
+        _native = module
+    return _native
 
 
 def _library():
@@ -199,6 +218,10 @@ def rms_norm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None,
     is fine), ``weight`` ``[d]`` of the same type, ``residual`` of ``x``'s shape
     in its type or in float32.  ``r`` has the residual's type and is ``x``
     itself without one; ``rstd`` is float32 ``[...]``."""
+    if stream is None and (_native or _native is None and _load_native()):
+        out = _native.rms_norm(x, weight, residual, eps, 0, 0)
+        if out is not None:
+            return out[0], out[2], out[3]
     y, _, r, rstd = _rms_forward(x, weight, residual, eps, None, 0, stream)
     return y, r, rstd
 
@@ -214,6 +237,10 @@ def rms_norm_quant(x: torch.Tensor, weight: torch.Tensor | None = None,
         raise ValueError(f"unknown kind {kind!r}; expected one of {sorted(_CODES)}")
     if group not in (0, 128):
         raise ValueError(f"group must be 0 or 128, got {group}")
+    if stream is None and (_native or _native is None and _load_native()):
+        out = _native.rms_norm(x, weight, residual, eps, _CODES[kind][0], group)
+        if out is not None:
+            return out
     return _rms_forward(x, weight, residual, eps, _CODES[kind], group, stream)
 
 
@@ -224,6 +251,10 @@ def rms_norm_adj(adj_y: torch.Tensor, r: torch.Tensor, rstd: torch.Tensor,
     gradient ``adj_y`` of ``y`` and, where something else reads ``r``, ``adj_r``
     of it.  ``adj_in`` (in ``r``'s type) is the gradient of the residual and of
     ``x`` alike; ``adj_weight`` is None without a weight or ``want_weight``."""
+    if stream is None and (_native or _native is None and _load_native()):
+        out = _native.rms_norm_adj(adj_y, r, rstd, weight, adj_r, want_weight)
+        if out is not None:
+            return out
     _model(adj_y, "adj_y")
     _model(r, "r")
     if r.shape != adj_y.shape:
@@ -343,6 +374,10 @@ def linrec_fwd(gate: torch.Tensor, x: torch.Tensor, state: torch.Tensor | None =
     ``S`` sequences one behind another, of any lengths, also none.  ``state``
     (float32 ``[B or S, D]``) is what each begins with, zeros by default; the
     returned one is what each ends with, not rounded to ``x``'s type."""
+    if stream is None and (_native or _native is None and _load_native()):
+        out = _native.linrec(gate, x, state, offsets, _GATES.get(kind, -1), complement)
+        if out is not None:
+            return out
     shape, strides, n = _recurrence(gate, x, state, offsets, kind)
     return _on(stream, (gate, x, state, offsets), _linrec_run, gate, x, state, offsets, _GATES[kind],
                bool(complement), shape, strides, n)
@@ -364,6 +399,10 @@ def linrec_step(gate: torch.Tensor, x: torch.Tensor, state: torch.Tensor, kind: 
                 complement: bool = True, stream=None):
     """One step for ``[B, D]`` gates and values: updates ``state`` (float32
     ``[B, D]``) in place and returns ``h`` ``[B, D]`` in ``x``'s type."""
+    if stream is None and (_native or _native is None and _load_native()):
+        out = _native.linrec_step(gate, x, state, _GATES.get(kind, -1), complement)
+        if out is not None:
+            return out
     if kind not in _GATES:
         raise ValueError(f"unknown kind {kind!r}; expected one of {sorted(_GATES)}")
     _model(x, "x")
@@ -401,6 +440,11 @@ def linrec_adj(gate: torch.Tensor, x: torch.Tensor, h: torch.Tensor, adj_h: torc
     gradients ``adj_h`` of ``h`` and ``adj_state`` of the final states (zeros by
     default).  ``h`` is the forward's output; ``adj_state0`` is the gradient of
     the initial states."""
+    if stream is None and (_native or _native is None and _load_native()):
+        out = _native.linrec_adj(gate, x, h, adj_h, state, adj_state, offsets, _GATES.get(kind, -1),
+                                 complement)
+        if out is not None:
+            return out
     shape, strides, n = _recurrence(gate, x, state, offsets, kind)
     adj_strides = _sequence(adj_h, "adj_h", offsets is not None, x)[3:]
     _model(h, "h", x)
@@ -497,6 +541,9 @@ class AdamW:
         if len(self.copies) != n:
             raise ValueError("copies must have an entry for each parameter")
         self._copied = any(c is not None for c in self.copies)
+        kinds = {c.dtype for c in self.copies if c is not None}
+        # the one type of the copies: -1 without any, None where they differ
+        self._copy_code = -1 if not kinds else _MODEL.get(kinds.pop()) if len(kinds) == 1 else None
         for i, p in enumerate(self.params):
             if not isinstance(p, torch.Tensor) or not p.is_cuda or p.dtype not in _PARAM:
                 raise ValueError(f"parameter {i} must be a CUDA tensor of a floating type of 16 "
@@ -519,6 +566,7 @@ class AdamW:
             if getattr(self, name) is not None:
                 t[name] = [x.data_ptr() for x in getattr(self, name)]
         t["copy"] = [0 if c is None else c.data_ptr() for c in self.copies]
+        self._table_at = t.ctypes.data
 
     def _new_state(self):
         """Zero moments: one allocation for each kind, tensors from 256 to 256."""
@@ -601,6 +649,13 @@ class AdamW:
         written (the step is still counted)."""
         params = self.params
         grads = [p.grad for p in params] if grads is None else list(grads)
+        if stream is None and self._copy_code is not None and \
+                (_native or _native is None and _load_native()):
+            if _native.adamw(params, grads, self._table_at, self._copy_code, self.state_bits,
+                             self.lr if lr is None else lr, self.betas[0], self.betas[1], self.eps,
+                             self.steps + 1, grad_scale, status):
+                self.steps += 1
+                return
         if len(grads) != len(params):
             raise ValueError("grads must have an entry for each parameter")
         if not params:
