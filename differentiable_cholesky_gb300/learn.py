@@ -23,6 +23,7 @@ import importlib.util
 
 import numpy as np
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import binding as _b
 
@@ -303,17 +304,23 @@ class _RmsNorm(torch.autograd.Function):
         y, r, rstd = rms_norm_fwd(x, weight, residual, eps)
         ctx.save_for_backward(r, rstd, weight)
         ctx.types = (x.dtype, residual is not None)
+        ctx.set_materialize_grads(False)
         if residual is None:
             r = x.new_empty(0)
             ctx.mark_non_differentiable(r)
         return y, r
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, adj_y, adj_r):
         r, rstd, weight = ctx.saved_tensors
         xtype, has_res = ctx.types
+        if adj_y is None:
+            if not has_res or adj_r is None:
+                return None, None, None, None
+            return adj_r.to(xtype), None, adj_r, None
         adj_in, adj_w = rms_norm_adj(adj_y.contiguous(), r, rstd, weight,
-                                     adj_r=adj_r.contiguous() if has_res else None,
+                                     adj_r=adj_r.contiguous() if has_res and adj_r is not None else None,
                                      want_weight=ctx.needs_input_grad[1])
         return adj_in.to(xtype), adj_w, adj_in if has_res else None, None
 
@@ -481,6 +488,7 @@ class _Linrec(torch.autograd.Function):
         return h, last
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, adj_h, adj_last):
         gate, x, h, state, offsets = ctx.saved_tensors
         if adj_h is None and adj_last is None:

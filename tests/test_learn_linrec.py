@@ -102,6 +102,20 @@ def test_packed_sequences(dtype, parts, d, comp):
     check(gate, x, None, off, "log", comp, zero_state=True)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("sequences", [3, 40, 1500])
+@pytest.mark.parametrize("d", [40, 33])
+def test_packed_sequences_over_many_tiles(dtype, sequences, d):
+    """A long axis, so that blocks walk several tiles: few sequences, some in
+    every tile, and more than one window of boundaries (many of them empty)."""
+    rng = np.random.default_rng(sequences)
+    cut = np.sort(rng.integers(0, 6001, sequences - 1))
+    cut[len(cut) // 2:len(cut) // 2 + sequences // 10] = cut[len(cut) // 2]  # a run of empty ones
+    off = torch.from_numpy(np.concatenate([[0], np.sort(cut), [6000]])).cuda()
+    gate, x = draw_gate((6000, d), dtype, 60, "log"), draw((6000, d), dtype, 61)
+    check(gate, x, draw((sequences, d), torch.float32, 62), off, "log", sequences % 2 == 0, seed=63)
+
+
 def test_sequences_do_not_see_one_another():
     """NaN and infinities of one packed sequence, and of its states, stay there."""
     from differentiable_cholesky_gb300 import learn

@@ -208,6 +208,23 @@ def test_autograd_with_mixed_types_and_without_residual():
     assert torch.isfinite(x2.grad).all()
 
 
+def test_autograd_with_one_output_used():
+    from differentiable_cholesky_gb300 import learn
+    x = draw((4, 96), torch.float32, 42).requires_grad_(True)
+    w = draw((96,), torch.float32, 43).requires_grad_(True)
+    res = draw((4, 96), torch.float32, 44).requires_grad_(True)
+    _, r = learn.rms_norm(x, w, res)
+    (r * 2).sum().backward()
+    assert torch.equal(x.grad, torch.full_like(x, 2)) and torch.equal(res.grad, x.grad) and w.grad is None
+    y, _ = learn.rms_norm(x, w, res)
+    y.sum().backward()
+    assert w.grad is not None
+    with pytest.raises(RuntimeError):  # no second derivative
+        y, _ = learn.rms_norm(x, w, res)
+        g, = torch.autograd.grad(y.square().sum(), x, create_graph=True)
+        g.sum().backward()
+
+
 def test_same_bits_each_time_and_in_place_residual():
     from differentiable_cholesky_gb300 import binding, learn
     x, w = draw((1500, 1024), torch.bfloat16, 50), draw((1024,), torch.bfloat16, 51)
