@@ -5,14 +5,15 @@
 //
 // Bound by memory: a pass moves 28 bytes an element with float32 parameters,
 // bf16 gradients and a bf16 copy (1.06 ms for 268M elements, 7.1 TB/s), 10
-// bytes with bf16 parameters and 8-bit moments (0.71 ms for 400M, 5.7 TB/s;
-// there the 45 instructions an element share the bound).  A warp does one
-// block and ends: more blocks a warp measured slower (4: 0.91 ms), and so did
-// fetching the next block ahead (1.0 ms), since both take registers, and what
-// hides the loads is many warps (12 blocks of 4 warps on an SM, 40 registers).
+// bytes with bf16 parameters and 8-bit moments (0.64 ms for 400M, 6.2 TB/s;
+// there the arithmetic takes nearly as long).  A warp does one block and ends:
+// more blocks a warp measured slower, and so did fetching the next block
+// ahead, since both take registers, and what hides the loads is many warps
+// (with 8-bit moments 9 to 11 thread blocks of 4 warps on an SM; 14 spill).
 //
 // The tensors' addresses and sizes travel in the kernel's parameters, so a
-// call needs no device table and no copy.  A warp takes a block of 256
+// call needs no device table and no copy; a thread block finds its tensor from
+// a hint for every so many thread blocks.  A warp takes a block of 256
 // consecutive elements of one tensor, eight a lane: with 8-bit moments such a
 // block shares one scale for m and one for sqrt(v), which the warp finds and
 // applies without leaving its registers.  8-bit moments are E4M3 values of
@@ -70,8 +71,10 @@ struct Scalars {
 // of thread blocks).
 template <int N>
 struct Table {
+    static constexpr int kHints = N > 64 ? 128 : 32;
     Scalars s;
-    int32_t count;
+    int32_t count, shift;
+    uint16_t hint[kHints];  // the entry of thread block h << shift
     uint32_t first[N + 1];
     Entry e[N];
 };
@@ -196,10 +199,10 @@ __device__ __forceinline__ float from_f64(uint32_t lo, uint32_t hi) {
     return __uint_as_float((hi & 0x80000000u) | t);
 }
 
-// sqrt(x) within 2^-22, for any x >= 0.
+// sqrt(x) within 2^-22, for x = 0 or x >= 2^-126 (0 for what is between).
 __device__ __forceinline__ float sqrt_near(float x) {
     float y;
-    asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 // Whether one of the four bytes is 0.
@@ -251,17 +254,24 @@ __device__ __forceinline__ void whole_block(const Scalars& s, const Entry& e, in
     // (two units of float32 in the update), and the codes where they
     // cannot be off (below)
     constexpr bool kExact = BITS == 32 || sizeof(P) == 8;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = kExact ? __fsqrt_rn(fv[i]) : sqrt_near(fv[i]);
     fill_v<8>(k, s.eps);
-    scale_v<8>(q, r, s.root);
-    add8(q, q, k);
     if constexpr (kExact) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] = __fsqrt_rn(fv[i]);
+        scale_v<8>(q, r, s.root);
+        add8(q, q, k);
 #pragma unroll
         for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(fm[i], q[i]);
     } else {
+        // (roots of v below 2^-126 are 0 here, which eps, at least 2^-36, hides)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = __fdividef(fm[i], q[i]);
+        for (int i = 0; i < 8; ++i) r[i] = sqrt_near(fv[i]);
+        float root[8];
+        fill_v<8>(root, s.root);
+        fma_v<8>(q, r, root, k);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = rcp_fast(q[i]);
+        mul_v<8>(q, q, fm);
     }
     scale_v<8>(q, q, -s.rate);  // what is added to the decayed parameter
     if constexpr (sizeof(P) == 8) {
@@ -305,7 +315,7 @@ __device__ __forceinline__ void whole_block(const Scalars& s, const Entry& e, in
             v.set(q);
             above.set(k);
             sure = v.w[0] == above.w[0] && v.w[1] == above.w[1];
-            // a code of 0 may be of a root above 0
+            // a code of 0 may be of a root above 0 (or of one that is not near)
             sure = sure && !zero_byte(v.w[0]) && !zero_byte(v.w[1]);
         } else {
             sure = false;
@@ -381,21 +391,19 @@ __device__ __noinline__ void any_block(const Scalars& s, const Entry& e, int64_t
 }
 
 template <typename P, typename G, int BITS, int N>
-__global__ void __launch_bounds__(kWarps * 32, BITS == 8 && sizeof(P) < 8 ? 12 : 1)
+__global__ void __launch_bounds__(kWarps * 32, BITS == 8 && sizeof(P) < 8 ? (sizeof(P) == 2 ? 11 : 9) : 1)
 adamw_kernel(const __grid_constant__ Table<N> tab) {
     if (tab.s.status != nullptr && *tab.s.status != 0) return;
-    // the entry with first[i] <= blockIdx.x < first[i + 1]
-    int lo = 0, hi = tab.count - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (tab.first[mid] <= blockIdx.x) lo = mid; else hi = mid - 1;
-    }
+    // the entry with first[lo] <= blockIdx.x < first[lo + 1], from a hint
+    int lo = tab.hint[blockIdx.x >> tab.shift];
+    while (tab.first[lo + 1] <= blockIdx.x) ++lo;
     const Entry& e = tab.e[lo];
     const float gs = tab.s.grad_scale != nullptr ? *tab.s.grad_scale : 1.0f;
     const int64_t block = (int64_t)(blockIdx.x - tab.first[lo]) * kWarps + threadIdx.x / 32;
     const int64_t at = block * kBlock;
     if (at >= e.numel) return;
-    if (e.vec && at + kBlock <= e.numel) whole_block<P, G, BITS>(tab.s, e, block, gs);
+    const bool near = BITS == 32 || sizeof(P) == 8 || tab.s.eps >= 0x1p-36f;
+    if (e.vec && near && at + kBlock <= e.numel) whole_block<P, G, BITS>(tab.s, e, block, gs);
     else any_block<P, G, BITS>(tab.s, e, block, at, gs);
 }
 
@@ -441,6 +449,12 @@ cudaError_t launch(int64_t count, const chol_adamw_tensor* t, const AdamwArgs& a
         }
         if (tab->count == 0) break;
         tab->first[tab->count] = (uint32_t)blocks;
+        tab->shift = 0;
+        while ((blocks - 1) >> tab->shift >= (uint64_t)Table<N>::kHints) ++tab->shift;
+        for (int h = 0, k = 0; h < Table<N>::kHints; ++h) {
+            while (k + 1 < tab->count && tab->first[k + 1] <= ((uint64_t)h << tab->shift)) ++k;
+            tab->hint[h] = (uint16_t)k;
+        }
         adamw_kernel<P, G, BITS, N><<<(unsigned)blocks, kWarps * 32, 0, stream>>>(*tab);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;

@@ -135,6 +135,29 @@ def test_against_the_formula_in_64_bits(ptype):
         assert np.all(off <= 3 * t * unit * (np.abs(p64) + moved) + (8 * t + 12) * R.U32 * moved)
 
 
+@pytest.mark.parametrize("eps,size", [(1e-8, 1e-21), (0.0, 1e-21), (1e-30, 1e-3), (0.0, 1e-3)])
+def test_small_eps_and_tiny_gradients_in_8_bits(eps, size):
+    """Second moments below the normal numbers, and an eps that hides nothing:
+    the same codes as one operation at a time gives."""
+    from differentiable_cholesky_gb300 import learn
+    rng = np.random.default_rng(8)
+    n = 2048
+    g = (rng.standard_normal(n) * size).astype(np.float32)
+    p = torch.from_numpy(rng.standard_normal(n).astype(np.float32)).cuda()
+    p0 = p.cpu().numpy()
+    opt = learn.AdamW([p], lr=LR, betas=BETAS, eps=eps, weight_decay=WD, state_bits=8)
+    opt.step([torch.from_numpy(g).cuda()])
+    zero = np.zeros(n, np.float32)
+    with np.errstate(divide="ignore", invalid="ignore"):
+        p1, m1, v1, r1 = R.adamw(p0, g, zero, zero, 8, LR, *BETAS, eps, WD, 1, 1.0)
+    for x, keep, q, s in ((m1, False, opt.m[0], opt.m_scale[0]), (r1, True, opt.v[0], opt.v_scale[0])):
+        want, ws = R.encode(x, keep)
+        assert torch.equal(s.cpu(), ws)
+        assert torch.equal(q.cpu().view(torch.uint8), want.view(torch.uint8))
+    upd = np.abs(p0 * np.float32(1.0 - LR * WD) - p1)
+    R.within(p, p1.astype(np.float64), 4 * R.U32 * upd + R.U32 * (np.abs(p0) + upd), torch.float32)
+
+
 def test_many_tensors_and_mixed_types():
     """More tensors than one launch carries, of three types; equal to one
     optimiser for each tensor."""
